@@ -3,8 +3,9 @@
 The compute lives in ``libgs.so`` (CUDA kernels for sm_100a behind the C ABI
 of ``include/gs.h``); ``binding`` marshals torch tensors to it and
 ``rasterizer`` drives the five stages for one camera.  ``scenes`` draws seeded
-synthetic inputs.
+synthetic inputs.  ``autograd`` is the differentiable interface (rasterizer,
+gated linear recurrence) and ``optim`` the gradient norm and clipping.
 """
 from . import scenes  # noqa: F401
 
-__all__ = ["scenes", "binding", "rasterizer", "build"]
+__all__ = ["scenes", "binding", "rasterizer", "autograd", "optim", "build"]

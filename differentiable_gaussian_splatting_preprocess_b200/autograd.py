@@ -1,4 +1,5 @@
-"""torch.autograd binding of the rasterizer: ``rasterize(...)`` returns the
+"""torch.autograd binding of the rasterizer and of the gated linear
+recurrence: ``rasterize(...)`` returns the
 image [3, H, W] of one camera and, when the graph is back-propagated, the
 gradients w.r.t. means, scales, quats, opacity and colours (the activated
 values the rasterizer consumes).  All work runs in libgs.so through a
@@ -9,6 +10,10 @@ transmittance, contributor counts, contribution mask) for the backward, so a
 Rasterizer must not run another forward before the backward of its previous
 one: use one Rasterizer per camera (as ``multiview`` does) when several views
 are rendered before one backward.
+
+``gated_scan(...)`` runs h_t = a_t h_{t-1} + x_t over sequences (its coupled
+form, back to front, composites ray samples) and ``scan_step(...)`` one row of
+it per kept state.
 """
 from __future__ import annotations
 
@@ -16,6 +21,7 @@ from typing import Optional
 
 import torch
 
+from . import binding as B
 from . import rasterizer as RZ
 
 
@@ -43,3 +49,92 @@ def rasterize(means: torch.Tensor, scales: torch.Tensor, quats: torch.Tensor, op
     bound for capacity mode (no host round trip); None sizes it from the
     frame's pair count."""
     return _Rasterize.apply(means, scales, quats, opacity, colors, rasterizer, capacity)
+
+
+def _evenly(t: torch.Tensor) -> torch.Tensor:
+    """The tensor itself where its rows are evenly spaced, else a contiguous copy."""
+    try:
+        B.row_stride(t)
+    except ValueError:
+        return t.contiguous()
+    return t
+
+
+def scan_workspace(a: torch.Tensor, x: torch.Tensor, seq_offsets: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """A workspace for gated_scan calls of these sizes (zero-filled uint8).
+    Calls that share one must not overlap on the GPU: keep one per stream, and
+    one per captured graph unless the graphs are replayed one after another."""
+    n = B.gs_scan_workspace_bytes(B.scan_desc(_evenly(a.detach()), _evenly(x.detach()), seq_offsets))
+    return torch.zeros(max(n, 16), dtype=torch.uint8, device=x.device)
+
+
+class _GatedScan(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, a, x, h0, seq_offsets, reverse, coupled, final_only, workspace):
+        a, x = _evenly(a), _evenly(x)
+        h0 = None if h0 is None else h0.contiguous()
+        d = B.scan_desc(a, x, seq_offsets)
+        if workspace is None:
+            need = B.gs_scan_workspace_bytes(d)
+            workspace = torch.zeros(need, dtype=torch.uint8, device=x.device) if need else None
+        h = None if final_only else torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        h_last = torch.empty((d.n_seq, d.channels), dtype=torch.float32, device=x.device)
+        states = None
+        if any(ctx.needs_input_grad[:3]):
+            states = torch.empty(B.gs_scan_states_bytes(d) // 4, dtype=torch.float32, device=x.device)
+        B.gs_scan_fwd(a, x, h, h_last, states, workspace, h0, seq_offsets, reverse, coupled,
+                      zero_pad=seq_offsets is not None)
+        ctx.save_for_backward(a, x, h0, seq_offsets, states)
+        ctx.mode, ctx.workspace = (reverse, coupled), workspace
+        ctx.set_materialize_grads(False)
+        return h, h_last
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dh, dh_last):
+        a, x, h0, seq_offsets, states = ctx.saved_tensors
+        reverse, coupled = ctx.mode
+        da = torch.empty(a.shape, dtype=a.dtype, device=a.device)
+        dx = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        dh0 = torch.empty_like(h0) if h0 is not None and ctx.needs_input_grad[2] else None
+        B.gs_scan_bwd(a, x, states, da, dx, None if dh is None else _evenly(dh),
+                      None if dh_last is None else dh_last.contiguous(), dh0, ctx.workspace, h0, seq_offsets, reverse,
+                      coupled, zero_pad=seq_offsets is not None)
+        return da, dx, dh0, None, None, None, None, None
+
+
+def gated_scan(a: torch.Tensor, x: torch.Tensor, h0: Optional[torch.Tensor] = None,
+               seq_offsets: Optional[torch.Tensor] = None, reverse: bool = False, coupled: bool = False,
+               final_only: bool = False, workspace: Optional[torch.Tensor] = None):
+    """h_t = a_t h_{t-1} + x_t along every sequence (``coupled``: a_t h_{t-1} +
+    (1 - a_t) x_t); returns (h, h_last).
+
+    ``x``: [rows, C] with ``seq_offsets`` (int64 [n_seq + 1], on the device;
+    None: one sequence), or [n_seq, rows, C]; float32, bfloat16 or float16.
+    ``a``: the same leading sizes and G gates a row, G dividing C (channel c
+    uses gate c // (C // G)); x's type or float32.  ``h0``: float32 [n_seq, C],
+    the state before each sequence (None: 0).  ``reverse`` runs from the last
+    row to the first.  ``h`` has x's shape and type (None with
+    ``final_only``); ``h_last`` is float32 [n_seq, C].  Rows outside
+    ``seq_offsets`` give zeros, in ``h`` and in the gradients.  Compositing of
+    samples listed front to back over a background: ``gated_scan(1 - alpha,
+    colour, h0=background, seq_offsets=..., reverse=True, coupled=True,
+    final_only=True)``.
+
+    Differentiable (once) w.r.t. ``a``, ``x`` and ``h0``.  ``workspace``: from
+    scan_workspace, kept by the caller across calls; the backward uses it
+    again.  None: one is made for the call."""
+    return _GatedScan.apply(a, x, h0, seq_offsets, reverse, coupled, final_only, workspace)
+
+
+def scan_step(a: torch.Tensor, x: torch.Tensor, state: torch.Tensor, out_state: Optional[torch.Tensor] = None,
+              coupled: bool = False):
+    """One row of gated_scan for each of n kept states: ``a`` [n, G], ``x`` [n,
+    C], ``state`` float32 [n, C]; returns (h of x's type, new state).  The new
+    state goes to ``out_state`` (which may be ``state``), or to a new tensor.
+    Not differentiable."""
+    a, x = _evenly(a.detach()), _evenly(x.detach())
+    out = torch.empty_like(state) if out_state is None else out_state
+    h = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    B.gs_scan_step(a, x, state.detach(), out, h, coupled)
+    return h, out

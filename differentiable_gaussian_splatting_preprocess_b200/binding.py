@@ -31,13 +31,19 @@ GS_ERR_OVERFLOW = 32
 GS_ERR_INDEX = 64
 GS_STAGE_PREPROCESS_FWD = 0
 GS_STAGE_BIN_SORT = 1
+GS_F32, GS_BF16, GS_F16 = 0, 1, 2
+GS_SCAN_REVERSE, GS_SCAN_COUPLED, GS_SCAN_ZERO_PAD = 1, 2, 4
+GS_NORM_L2, GS_NORM_INF = 0, 1
 TILE = 16
+DTYPE_CODE = {torch.float32: GS_F32, torch.bfloat16: GS_BF16, torch.float16: GS_F16}
 
 # Every symbol include/gs.h declares.
 EXPORTED = ("gs_version", "gs_launch_count", "gs_status_string", "gs_workspace_bytes", "gs_read_status", "gs_clear_status",
             "gs_preprocess_fwd", "gs_bin_sort", "gs_render_fwd", "gs_render_bwd", "gs_preprocess_bwd",
             "gs_preprocess_fwd_noalloc", "gs_render_stats", "gs_sh_fwd", "gs_sh_bwd", "gs_sh_fwd_f16",
-            "gs_sh_bwd_f16", "gs_adam_step", "gs_debug_configure", "gs_debug_read")
+            "gs_sh_bwd_f16", "gs_adam_step", "gs_adam_step_clipped", "gs_scan_workspace_bytes", "gs_scan_states_bytes",
+            "gs_scan_fwd", "gs_scan_bwd", "gs_scan_step", "gs_grad_norm_workspace_bytes", "gs_grad_norm",
+            "gs_grad_clip", "gs_debug_configure", "gs_debug_read")
 
 
 class GsCamera(ctypes.Structure):
@@ -58,6 +64,21 @@ class GsAdamConfig(ctypes.Structure):
     _fields_ = [("lr_means", ctypes.c_float), ("lr_scales", ctypes.c_float), ("lr_quats", ctypes.c_float),
                 ("lr_opacity", ctypes.c_float), ("lr_colors", ctypes.c_float), ("beta1", ctypes.c_float),
                 ("beta2", ctypes.c_float), ("eps", ctypes.c_float), ("warmup_steps", ctypes.c_int)]
+
+
+class GsScanDesc(ctypes.Structure):
+    """Mirror of ``gs_scan_desc`` in include/gs.h."""
+    _fields_ = [("rows", ctypes.c_longlong), ("channels", ctypes.c_int), ("gates", ctypes.c_int),
+                ("n_seq", ctypes.c_int), ("dtype", ctypes.c_int), ("gate_dtype", ctypes.c_int),
+                ("flags", ctypes.c_int), ("stride_a", ctypes.c_longlong), ("stride_x", ctypes.c_longlong),
+                ("stride_h", ctypes.c_longlong), ("stride_da", ctypes.c_longlong), ("stride_dx", ctypes.c_longlong),
+                ("stride_dh", ctypes.c_longlong)]
+
+
+class GsTensorList(ctypes.Structure):
+    """Mirror of ``gs_tensor_list`` in include/gs.h (host arrays)."""
+    _fields_ = [("count", ctypes.c_int), ("data", ctypes.POINTER(ctypes.c_void_p)),
+                ("numel", ctypes.POINTER(ctypes.c_longlong)), ("dtype", ctypes.POINTER(ctypes.c_int))]
 
 
 class GsError(RuntimeError):
@@ -109,6 +130,26 @@ def lib() -> ctypes.CDLL:
         L.gs_preprocess_fwd_noalloc.argtypes = [cam, I] + [P] * 11 + [P]
         L.gs_adam_step.restype = I
         L.gs_adam_step.argtypes = [ctypes.POINTER(GsAdamConfig), I, I, I] + [P] * 14 + [P]
+        F = ctypes.c_float
+        L.gs_adam_step_clipped.restype = I
+        L.gs_adam_step_clipped.argtypes = [ctypes.POINTER(GsAdamConfig), I, I, I] + [P] * 14 + [P, F, F, P]
+        desc, tlist = ctypes.POINTER(GsScanDesc), ctypes.POINTER(GsTensorList)
+        L.gs_scan_workspace_bytes.restype = S
+        L.gs_scan_workspace_bytes.argtypes = [desc]
+        L.gs_scan_states_bytes.restype = S
+        L.gs_scan_states_bytes.argtypes = [desc]
+        L.gs_scan_fwd.restype = I
+        L.gs_scan_fwd.argtypes = [desc] + [P] * 8 + [S, P]
+        L.gs_scan_bwd.restype = I
+        L.gs_scan_bwd.argtypes = [desc] + [P] * 11 + [S, P]
+        L.gs_scan_step.restype = I
+        L.gs_scan_step.argtypes = [desc] + [P] * 6
+        L.gs_grad_norm_workspace_bytes.restype = S
+        L.gs_grad_norm_workspace_bytes.argtypes = []
+        L.gs_grad_norm.restype = I
+        L.gs_grad_norm.argtypes = [tlist, I, P, P, S, P]
+        L.gs_grad_clip.restype = I
+        L.gs_grad_clip.argtypes = [tlist, ctypes.POINTER(P), P, F, F, P]
         L.gs_sh_fwd_f16.restype = I
         L.gs_sh_fwd_f16.argtypes = [cam, I, I, I, P, P, ctypes.c_float, P, P]
         L.gs_sh_bwd_f16.restype = I
@@ -448,14 +489,8 @@ def gs_preprocess_fwd_noalloc(cam, means, scales, quats, opacity, mean2d, depth,
         _ptr(conic_opacity), _ptr(radius), _ptr(rect), _ptr(tiles_touched), _ptr(d_num_pairs), _stream(stream)))
 
 
-def gs_adam_step(cfg: GsAdamConfig, step: int, params: dict, grads: dict, m, v, scales=None, opacity=None,
-                 stream=None) -> None:
-    """Fused Adam step.  ``params``: means [N,3], log_scales [N,3], quats [N,4],
-    logit_opacity [N], colors [N,C] (float32, updated in place); ``grads``:
-    dL_dmeans, dL_dscales, dL_dquats, dL_dopacity, dL_dcolors as returned by
-    the rasterizer (w.r.t. activated scales and opacity); ``m``, ``v``: float32
-    [(11 + C) N] moments (zero before step 1); ``scales``, ``opacity``:
-    optional outputs of the new activated values."""
+def _check_adam(params: dict, grads: dict, m, v, scales, opacity) -> tuple:
+    """Checks the tensors of an Adam step; returns (N, C)."""
     N = params["means"].shape[0]
     colors = params["colors"]
     C = colors.shape[1] if colors.dim() == 2 else int(colors[0].numel()) if N else 0
@@ -470,8 +505,231 @@ def gs_adam_step(cfg: GsAdamConfig, step: int, params: dict, grads: dict, m, v, 
     _check(v, "v", f32, ((11 + C) * N,))
     _check(scales, "scales", f32, (N, 3), optional=True)
     _check(opacity, "opacity", f32, (N,), optional=True)
+    return int(N), int(C)
+
+
+def gs_adam_step(cfg: GsAdamConfig, step: int, params: dict, grads: dict, m, v, scales=None, opacity=None,
+                 stream=None) -> None:
+    """Fused Adam step.  ``params``: means [N,3], log_scales [N,3], quats [N,4],
+    logit_opacity [N], colors [N,C] (float32, updated in place); ``grads``:
+    dL_dmeans, dL_dscales, dL_dquats, dL_dopacity, dL_dcolors as returned by
+    the rasterizer (w.r.t. activated scales and opacity); ``m``, ``v``: float32
+    [(11 + C) N] moments (zero before step 1); ``scales``, ``opacity``:
+    optional outputs of the new activated values."""
+    N, C = _check_adam(params, grads, m, v, scales, opacity)
     _ok("gs_adam_step", lib().gs_adam_step(
         ctypes.byref(cfg), int(step), int(N), int(C), _ptr(params["means"]), _ptr(params["log_scales"]),
-        _ptr(params["quats"]), _ptr(params["logit_opacity"]), _ptr(colors), _ptr(grads["dL_dmeans"]),
+        _ptr(params["quats"]), _ptr(params["logit_opacity"]), _ptr(params["colors"]), _ptr(grads["dL_dmeans"]),
         _ptr(grads["dL_dscales"]), _ptr(grads["dL_dquats"]), _ptr(grads["dL_dopacity"]), _ptr(grads["dL_dcolors"]),
         _ptr(m), _ptr(v), _ptr(scales), _ptr(opacity), _stream(stream)))
+
+
+def gs_adam_step_clipped(cfg: GsAdamConfig, step: int, params: dict, grads: dict, m, v, grad_norm, max_norm: float,
+                         scales=None, opacity=None, clip_eps: float = 1e-6, stream=None) -> None:
+    """gs_adam_step on the gradients scaled by min(1, max_norm / (grad_norm +
+    clip_eps)); ``grad_norm``: one float32 on the device."""
+    _check(grad_norm, "grad_norm", torch.float32, (1,))
+    N, C = _check_adam(params, grads, m, v, scales, opacity)
+    _same_device(m, [grad_norm])
+    with _on_device(m, stream) as s:
+        _ok("gs_adam_step_clipped", lib().gs_adam_step_clipped(
+            ctypes.byref(cfg), int(step), N, C, _ptr(params["means"]), _ptr(params["log_scales"]),
+            _ptr(params["quats"]), _ptr(params["logit_opacity"]), _ptr(params["colors"]), _ptr(grads["dL_dmeans"]),
+            _ptr(grads["dL_dscales"]), _ptr(grads["dL_dquats"]), _ptr(grads["dL_dopacity"]),
+            _ptr(grads["dL_dcolors"]), _ptr(m), _ptr(v), _ptr(scales), _ptr(opacity), _ptr(grad_norm),
+            float(max_norm), float(clip_eps), s))
+
+
+class _on_device:
+    """The tensor's device made current for a launch, with the stream to
+    launch on (``stream``, or that device's current one)."""
+
+    def __init__(self, t: torch.Tensor, stream=None):
+        self.index, self.stream, self.guard = t.device.index, stream, None
+
+    def __enter__(self) -> ctypes.c_void_p:
+        if torch.cuda.current_device() != self.index:
+            self.guard = torch.cuda.device(self.index)
+            self.guard.__enter__()
+        return _stream(self.stream)
+
+    def __exit__(self, *exc):
+        if self.guard is not None:
+            self.guard.__exit__(*exc)
+
+
+def _same_device(t: torch.Tensor, others) -> None:
+    for o in others:
+        if o is not None and o.device != t.device:
+            raise ValueError(f"tensors are on different devices ({t.device} and {o.device})")
+
+
+def row_stride(t: torch.Tensor, name: str = "tensor") -> int:
+    """Elements between neighbouring rows of a [rows, n] or [batch, rows, n]
+    tensor whose rows are evenly spaced and contiguous inside; raises
+    ValueError for any other layout."""
+    n = t.shape[-1]
+    if t.dim() not in (2, 3):
+        raise ValueError(f"{name} must have 2 or 3 dimensions, got {t.dim()}")
+    rows = t.shape[0] if t.dim() == 2 else t.shape[0] * t.shape[1]
+    if t.numel() == 0 or rows == 1:
+        step = n
+    elif t.dim() == 2 or t.shape[0] == 1:
+        step = t.stride(-2)
+    elif t.shape[1] == 1:
+        step = t.stride(0)
+    else:
+        step = t.stride(1)
+        if t.stride(0) != t.shape[1] * step:
+            step = -1
+    if step < n or (n > 1 and t.stride(-1) != 1 and t.numel() > 0):
+        raise ValueError(f"{name} must have evenly spaced rows of contiguous elements")
+    return step
+
+
+def scan_desc(a, x, seq_offsets=None, reverse: bool = False, coupled: bool = False, zero_pad: bool = False,
+              h=None, dL_da=None, dL_dx=None, dL_dh=None) -> GsScanDesc:
+    """The gs_scan_desc of gates ``a`` and inputs ``x``: [rows, C] with
+    ``seq_offsets`` (int64 [n_seq + 1]; None: one sequence), or [n_seq, rows,
+    C] for sequences of equal length.  ``a`` has the same leading sizes and a
+    number of gates that divides C."""
+    for t, name in ((a, "a"), (x, "x")):
+        if not t.is_cuda:
+            raise ValueError(f"{name} must be a CUDA tensor")
+        if t.dtype not in DTYPE_CODE:
+            raise ValueError(f"{name} must be float32, bfloat16 or float16, got {t.dtype}")
+    if a.dtype not in (x.dtype, torch.float32):
+        raise ValueError(f"a must be float32 or {x.dtype}, got {a.dtype}")
+    if x.dim() not in (2, 3) or a.shape[:-1] != x.shape[:-1]:
+        raise ValueError(f"a and x must have equal leading sizes, got {tuple(a.shape)} and {tuple(x.shape)}")
+    C, G = x.shape[-1], a.shape[-1]
+    if C < 1 or G < 1 or C % G:
+        raise ValueError(f"the number of gates ({G}) must divide the number of channels ({C})")
+    d = GsScanDesc()
+    if x.dim() == 3:
+        if seq_offsets is not None:
+            raise ValueError("seq_offsets goes with x of shape [rows, C]")
+        d.n_seq, d.rows = x.shape[0], x.shape[0] * x.shape[1]
+    else:
+        d.rows = x.shape[0]
+        d.n_seq = 1
+        if seq_offsets is not None:
+            _check(seq_offsets, "seq_offsets", torch.int64)
+            if seq_offsets.dim() != 1 or seq_offsets.numel() < 2:
+                raise ValueError("seq_offsets must be [n_seq + 1] with n_seq >= 1")
+            d.n_seq = seq_offsets.numel() - 1
+    d.channels, d.gates = C, G
+    d.dtype, d.gate_dtype = DTYPE_CODE[x.dtype], DTYPE_CODE[a.dtype]
+    d.flags = ((GS_SCAN_REVERSE if reverse else 0) | (GS_SCAN_COUPLED if coupled else 0)
+               | (GS_SCAN_ZERO_PAD if zero_pad else 0))
+    d.stride_a, d.stride_x = row_stride(a, "a"), row_stride(x, "x")
+    for t, ref, name, field in ((h, x, "h", "stride_h"), (dL_da, a, "dL_da", "stride_da"),
+                                (dL_dx, x, "dL_dx", "stride_dx"), (dL_dh, x, "dL_dh", "stride_dh")):
+        if t is None:
+            setattr(d, field, ref.shape[-1])
+            continue
+        if t.dtype != ref.dtype or t.shape != ref.shape:
+            raise ValueError(f"{name} must be {ref.dtype} of shape {tuple(ref.shape)}, got {t.dtype} {tuple(t.shape)}")
+        setattr(d, field, row_stride(t, name))
+    return d
+
+
+def gs_scan_workspace_bytes(desc: GsScanDesc) -> int:
+    return int(lib().gs_scan_workspace_bytes(ctypes.byref(desc)))
+
+
+def gs_scan_states_bytes(desc: GsScanDesc) -> int:
+    return int(lib().gs_scan_states_bytes(ctypes.byref(desc)))
+
+
+def _check_scan_states(desc: GsScanDesc, states, ws, **per_seq) -> None:
+    for name, t in per_seq.items():
+        _check(t, name, torch.float32, (desc.n_seq, desc.channels), optional=True)
+    _check(states, "states", torch.float32, optional=True)
+    if states is not None and 4 * states.numel() < gs_scan_states_bytes(desc):
+        raise ValueError("states holds fewer bytes than gs_scan_states_bytes(desc)")
+    _check(ws, "ws", torch.uint8, optional=True)
+
+
+def gs_scan_fwd(a, x, h=None, h_last=None, states=None, ws=None, h0=None, seq_offsets=None, reverse: bool = False,
+                coupled: bool = False, zero_pad: bool = False, stream=None) -> None:
+    """Gated linear recurrence; see scan_desc for ``a``, ``x`` and
+    ``seq_offsets``.  Writes ``h`` (x's type and shape), ``h_last`` [n_seq, C]
+    float32 and ``states`` (float32, gs_scan_states_bytes) where given."""
+    d = scan_desc(a, x, seq_offsets, reverse, coupled, zero_pad, h=h)
+    _check_scan_states(d, states, ws, h0=h0, h_last=h_last)
+    _same_device(x, (a, h, h_last, states, ws, h0, seq_offsets))
+    with _on_device(x, stream) as s:
+        _ok("gs_scan_fwd", lib().gs_scan_fwd(
+            ctypes.byref(d), _ptr(a), _ptr(x), _ptr(h0), _ptr(seq_offsets), _ptr(h), _ptr(h_last), _ptr(states),
+            _ptr(ws), 0 if ws is None else ws.numel(), s))
+
+
+def gs_scan_bwd(a, x, states, dL_da, dL_dx, dL_dh=None, dL_dh_last=None, dL_dh0=None, ws=None, h0=None,
+                seq_offsets=None, reverse: bool = False, coupled: bool = False, zero_pad: bool = False,
+                stream=None) -> None:
+    """Gradients of gs_scan_fwd's inputs (written): ``dL_da``, ``dL_dx`` and,
+    where given, ``dL_dh0``, from ``dL_dh`` and ``dL_dh_last`` (None: zero) and
+    the forward's ``states``."""
+    d = scan_desc(a, x, seq_offsets, reverse, coupled, zero_pad, dL_da=dL_da, dL_dx=dL_dx, dL_dh=dL_dh)
+    if states is None:
+        raise ValueError("states is required")
+    _check_scan_states(d, states, ws, h0=h0, dL_dh_last=dL_dh_last, dL_dh0=dL_dh0)
+    _same_device(x, (a, dL_da, dL_dx, dL_dh, dL_dh_last, dL_dh0, states, ws, h0, seq_offsets))
+    with _on_device(x, stream) as s:
+        _ok("gs_scan_bwd", lib().gs_scan_bwd(
+            ctypes.byref(d), _ptr(a), _ptr(x), _ptr(h0), _ptr(seq_offsets), _ptr(states), _ptr(dL_dh),
+            _ptr(dL_dh_last), _ptr(dL_da), _ptr(dL_dx), _ptr(dL_dh0), _ptr(ws), 0 if ws is None else ws.numel(), s))
+
+
+def gs_scan_step(a, x, state, state_out, h=None, coupled: bool = False, stream=None) -> None:
+    """One row of the recurrence per kept state: ``a`` [n, G], ``x`` [n, C],
+    ``state`` and ``state_out`` [n, C] float32 (may be the same tensor),
+    ``h`` [n, C] of x's type or None."""
+    if x.dim() != 2:
+        raise ValueError("x must have shape [n, C]")
+    d = scan_desc(a, x, coupled=coupled, h=h)
+    d.n_seq = d.rows
+    _check(state, "state", torch.float32, tuple(x.shape))
+    _check(state_out, "state_out", torch.float32, tuple(x.shape))
+    _same_device(x, (a, state, state_out, h))
+    with _on_device(x, stream) as s:
+        _ok("gs_scan_step", lib().gs_scan_step(ctypes.byref(d), _ptr(a), _ptr(x), _ptr(state), _ptr(state_out),
+                                               _ptr(h), s))
+
+
+def tensor_list(tensors) -> tuple:
+    """(gs_tensor_list, pointer array) of contiguous CUDA tensors of one
+    device; the caller keeps the tensors alive."""
+    n = len(tensors)
+    for i, t in enumerate(tensors):
+        if not t.is_cuda or t.dtype not in DTYPE_CODE or not t.is_contiguous():
+            raise ValueError(f"tensor {i} must be a contiguous float32, bfloat16 or float16 CUDA tensor")
+    if n:
+        _same_device(tensors[0], tensors[1:])
+    data = (ctypes.c_void_p * max(n, 1))(*[t.data_ptr() for t in tensors])
+    numel = (ctypes.c_longlong * max(n, 1))(*[t.numel() for t in tensors])
+    dtype = (ctypes.c_int * max(n, 1))(*[DTYPE_CODE[t.dtype] for t in tensors])
+    return GsTensorList(n, data, numel, dtype), data
+
+
+def gs_grad_norm_workspace_bytes() -> int:
+    return int(lib().gs_grad_norm_workspace_bytes())
+
+
+def gs_grad_norm(tlist: GsTensorList, norm, ws, kind: int = GS_NORM_L2, stream=None) -> None:
+    """``norm`` [1] float32 = the norm over the tensors of ``tlist``
+    (tensor_list); ``ws``: uint8, zero-filled once."""
+    _check(norm, "norm", torch.float32, (1,))
+    _check(ws, "ws", torch.uint8)
+    with _on_device(norm, stream) as s:
+        _ok("gs_grad_norm", lib().gs_grad_norm(ctypes.byref(tlist), int(kind), _ptr(norm), _ptr(ws), ws.numel(), s))
+
+
+def gs_grad_clip(tlist: GsTensorList, norm, max_norm: float, dst=None, eps: float = 1e-6, stream=None) -> None:
+    """Scales the tensors of ``tlist`` by min(1, max_norm / (norm + eps)), into
+    the tensors of ``dst`` (a pointer array of tensor_list, in the same order
+    and of the same sizes and types) or in place."""
+    _check(norm, "norm", torch.float32, (1,))
+    with _on_device(norm, stream) as s:
+        _ok("gs_grad_clip", lib().gs_grad_clip(ctypes.byref(tlist), dst, _ptr(norm), float(max_norm), float(eps), s))

@@ -27,6 +27,8 @@ struct AdamRates {
     float inv_bc1;     // 1 / (1 - b1^t)
     float inv_bc2;     // 1 / (1 - b2^t)
     float b1, b2, eps;
+    const float* grad_norm;  // one value on the device, or NULL: gradients as they are
+    float max_norm, clip_eps;
 };
 
 __device__ __forceinline__ float adam_update(float p, float g, float& m, float& v, float rate, const AdamRates& r) {
@@ -50,13 +52,18 @@ k_adam(int N, int C, AdamRates r, float* __restrict__ means, float* __restrict__
     const size_t e_means = 3 * n, e_scales = 6 * n, e_op = 7 * n, e_col = 7 * n + (size_t)C * n, e_all = e_col + n;
     const size_t o_scales = 3 * n, o_quats = 6 * n, o_op = 10 * n, o_col = 11 * n;
     const size_t stride = (size_t)gridDim.x * blockDim.x;
+    float coef = 1.0f;
+    if (r.grad_norm) {
+        const float q = r.max_norm / (*r.grad_norm + r.clip_eps);
+        coef = q > 1.0f ? 1.0f : q;  // a NaN stays
+    }
     for (size_t i = (size_t)blockIdx.x * blockDim.x + threadIdx.x; i < e_all; i += stride) {
         if (i < e_means) {
-            means[i] = adam_update(means[i], g_means[i], m[i], v[i], r.rate[0], r);
+            means[i] = adam_update(means[i], coef * g_means[i], m[i], v[i], r.rate[0], r);
         } else if (i < e_scales) {
             const size_t k = i - e_means;
             const float ls = log_scales[k];
-            const float g = g_scales[k] * expf(ls);  // d exp(x) / dx
+            const float g = coef * g_scales[k] * expf(ls);  // d exp(x) / dx
             const float nls = adam_update(ls, g, m[o_scales + k], v[o_scales + k], r.rate[1], r);
             log_scales[k] = nls;
             if (scales_out) scales_out[k] = expf(nls);
@@ -64,23 +71,23 @@ k_adam(int N, int C, AdamRates r, float* __restrict__ means, float* __restrict__
             const size_t k = i - e_scales;
             const float x = logit_opacity[k];
             const float o = 1.0f / (1.0f + expf(-x));
-            const float g = g_opacity[k] * o * (1.0f - o);  // d sigmoid(x) / dx
+            const float g = coef * g_opacity[k] * o * (1.0f - o);  // d sigmoid(x) / dx
             const float nx = adam_update(x, g, m[o_op + k], v[o_op + k], r.rate[3], r);
             logit_opacity[k] = nx;
             if (opacity_out) opacity_out[k] = 1.0f / (1.0f + expf(-nx));
         } else if (i < e_col) {
             const size_t k = i - e_op;
-            colors[k] = adam_update(colors[k], g_colors[k], m[o_col + k], v[o_col + k], r.rate[4], r);
+            colors[k] = adam_update(colors[k], coef * g_colors[k], m[o_col + k], v[o_col + k], r.rate[4], r);
         } else {
             const size_t k = i - e_col;
             float4 q = quats[k];
             const float4 g = g_quats[k];
             float* mq = m + o_quats + 4 * k;
             float* vq = v + o_quats + 4 * k;
-            q.x = adam_update(q.x, g.x, mq[0], vq[0], r.rate[2], r);
-            q.y = adam_update(q.y, g.y, mq[1], vq[1], r.rate[2], r);
-            q.z = adam_update(q.z, g.z, mq[2], vq[2], r.rate[2], r);
-            q.w = adam_update(q.w, g.w, mq[3], vq[3], r.rate[2], r);
+            q.x = adam_update(q.x, coef * g.x, mq[0], vq[0], r.rate[2], r);
+            q.y = adam_update(q.y, coef * g.y, mq[1], vq[1], r.rate[2], r);
+            q.z = adam_update(q.z, coef * g.z, mq[2], vq[2], r.rate[2], r);
+            q.w = adam_update(q.w, coef * g.w, mq[3], vq[3], r.rate[2], r);
             const float nn = q.x * q.x + q.y * q.y + q.z * q.z + q.w * q.w;
             if (nn > 0.0f) {
                 const float inv = rsqrtf(nn);
@@ -91,16 +98,11 @@ k_adam(int N, int C, AdamRates r, float* __restrict__ means, float* __restrict__
     }
 }
 
-}  // namespace
-}  // namespace gs
-
-using namespace gs;
-
-extern "C" int gs_adam_step(const gs_adam_config* cfg, int step, int N, int C, float* means, float* log_scales,
-                            float* quats, float* logit_opacity, float* colors, const float* dL_dmeans,
-                            const float* dL_dscales, const float* dL_dquats, const float* dL_dopacity,
-                            const float* dL_dcolors, float* m, float* v, float* scales, float* opacity,
-                            void* stream) {
+int adam_launch(const gs_adam_config* cfg, int step, int N, int C, float* means, float* log_scales, float* quats,
+                float* logit_opacity, float* colors, const float* dL_dmeans, const float* dL_dscales,
+                const float* dL_dquats, const float* dL_dopacity, const float* dL_dcolors, float* m, float* v,
+                float* scales, float* opacity, const float* grad_norm, float max_norm, float clip_eps,
+                void* stream) {
     if (!cfg || step < 1 || N < 0 || C < 0) return GS_ERR_INVALID_ARG;
     if (!(cfg->beta1 >= 0.0f && cfg->beta1 < 1.0f && cfg->beta2 >= 0.0f && cfg->beta2 < 1.0f && cfg->eps >= 0.0f))
         return GS_ERR_INVALID_ARG;
@@ -119,6 +121,9 @@ extern "C" int gs_adam_step(const gs_adam_config* cfg, int step, int N, int C, f
     r.b1 = cfg->beta1;
     r.b2 = cfg->beta2;
     r.eps = cfg->eps;
+    r.grad_norm = grad_norm;
+    r.max_norm = max_norm;
+    r.clip_eps = clip_eps;
     const size_t items = (size_t)N * (8 + (size_t)C);
     size_t blocks = (items + kAdamBlock - 1) / kAdamBlock;
     if (blocks > 148u * 16u) blocks = 148u * 16u;
@@ -127,4 +132,30 @@ extern "C" int gs_adam_step(const gs_adam_config* cfg, int step, int N, int C, f
         reinterpret_cast<const float4*>(dL_dquats), dL_dopacity, dL_dcolors, m, v, scales, opacity); note_launch();
     GS_LAUNCH_CHECK();
     return GS_OK;
+}
+
+}  // namespace
+}  // namespace gs
+
+using namespace gs;
+
+extern "C" int gs_adam_step(const gs_adam_config* cfg, int step, int N, int C, float* means, float* log_scales,
+                            float* quats, float* logit_opacity, float* colors, const float* dL_dmeans,
+                            const float* dL_dscales, const float* dL_dquats, const float* dL_dopacity,
+                            const float* dL_dcolors, float* m, float* v, float* scales, float* opacity,
+                            void* stream) {
+    return adam_launch(cfg, step, N, C, means, log_scales, quats, logit_opacity, colors, dL_dmeans, dL_dscales,
+                       dL_dquats, dL_dopacity, dL_dcolors, m, v, scales, opacity, nullptr, 0.0f, 0.0f, stream);
+}
+
+extern "C" int gs_adam_step_clipped(const gs_adam_config* cfg, int step, int N, int C, float* means,
+                                    float* log_scales, float* quats, float* logit_opacity, float* colors,
+                                    const float* dL_dmeans, const float* dL_dscales, const float* dL_dquats,
+                                    const float* dL_dopacity, const float* dL_dcolors, float* m, float* v,
+                                    float* scales, float* opacity, const float* grad_norm, float max_norm,
+                                    float clip_eps, void* stream) {
+    if (!grad_norm || !aligned(grad_norm, 4) || !(max_norm >= 0.0f) || !(clip_eps >= 0.0f)) return GS_ERR_INVALID_ARG;
+    return adam_launch(cfg, step, N, C, means, log_scales, quats, logit_opacity, colors, dL_dmeans, dL_dscales,
+                       dL_dquats, dL_dopacity, dL_dcolors, m, v, scales, opacity, grad_norm, max_norm, clip_eps,
+                       stream);
 }

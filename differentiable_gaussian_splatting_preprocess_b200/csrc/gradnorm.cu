@@ -1,0 +1,328 @@
+// Norm over a list of gradient tensors, and clipping by it.
+//
+// The tensors are cut into chunks of kChunk elements (each tensor starts a
+// new one); a block finds a chunk's tensor by a search in the launch's own
+// parameters, which hold the list: no copy to the device, nothing kept
+// between calls.  The norm's blocks each leave one partial (64-bit sum of
+// squares, or largest magnitude); the call's last block joins them in a
+// fixed order.
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include "gs_internal.cuh"
+
+namespace gs {
+namespace {
+
+constexpr int kNormBlock = 256;
+constexpr int kChunk = 16384;               // elements
+constexpr int kMaxGrid = 148 * 8;           // blocks of one launch
+constexpr int kSmallList = 32, kLargeList = 960;
+
+struct Entry {
+    const void* src;
+    void* dst;
+    long long numel;
+    unsigned first;   // first chunk of this tensor in the launch
+    int dtype;
+};
+
+template <int N> struct Entries {
+    int count;
+    unsigned chunks;
+    Entry e[N];
+};
+
+struct NormScratch {
+    unsigned ticket;
+    unsigned pad[63];
+    double part[kMaxGrid];
+};
+
+// Sum of squares of the values, as a 64-bit value.  The fp32 sum serves
+// unless it left the range in which squares are exact enough: then the values
+// are scaled by a power of two first (2^-64 or 2^64), which loses nothing.
+template <int N> __device__ __forceinline__ double square_sum(const float (&f)[N]) {
+    float s = 0.0f;
+#pragma unroll
+    for (int i = 0; i < N; ++i) s = fmaf(f[i], f[i], s);
+    if (s > 1e-26f && s < 3e38f) return (double)s;
+    const float k = s > 1.0f ? 0x1p-64f : 0x1p+64f;
+    const double back = s > 1.0f ? 0x1p+128 : 0x1p-128;
+    s = 0.0f;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        const float v = f[i] * k;
+        s = fmaf(v, v, s);
+    }
+    return (double)s * back;
+}
+
+// 16 bytes of a tensor as fp32 values.
+template <typename T> struct Vec16 {
+    static constexpr int n = 16 / sizeof(T);
+    __device__ static __forceinline__ void unpack(uint4 w, float (&f)[n]) {
+        T t[n];
+        memcpy(t, &w, 16);
+#pragma unroll
+        for (int i = 0; i < n; ++i) {
+            if constexpr (sizeof(T) == 4) f[i] = t[i];
+            else f[i] = (float)t[i];
+        }
+    }
+    __device__ static __forceinline__ uint4 pack(const float (&f)[n]) {
+        T t[n];
+#pragma unroll
+        for (int i = 0; i < n; ++i) t[i] = (T)f[i];
+        uint4 w;
+        memcpy(&w, t, 16);
+        return w;
+    }
+};
+
+// One chunk [b, e) of a tensor: a head up to the first 16-byte boundary and
+// a tail element by element, 16-byte pieces between them.
+template <typename T, typename One, typename Many>
+__device__ __forceinline__ void walk(const T* g, long long b, long long e, One one, Many many) {
+    constexpr int n = 16 / sizeof(T);
+    long long vb = b + (long long)((16 - ((uintptr_t)(g + b) & 15)) & 15) / (long long)sizeof(T);
+    if (vb > e) vb = e;
+    const int vecs = (int)((e - vb) / n);
+    for (long long i = b + threadIdx.x; i < vb; i += kNormBlock) one(i);
+    constexpr int kUnroll = 4;
+    int i = threadIdx.x;
+    for (; i + (kUnroll - 1) * kNormBlock < vecs; i += kUnroll * kNormBlock) {
+        uint4 w[kUnroll];
+#pragma unroll
+        for (int u = 0; u < kUnroll; ++u)
+            w[u] = __ldcs(reinterpret_cast<const uint4*>(g + vb) + i + u * kNormBlock);
+#pragma unroll
+        for (int u = 0; u < kUnroll; ++u) many(vb + (long long)(i + u * kNormBlock) * n, w[u]);
+    }
+    for (; i < vecs; i += kNormBlock)
+        many(vb + (long long)i * n, __ldcs(reinterpret_cast<const uint4*>(g + vb) + i));
+    for (long long j = vb + (long long)vecs * n + threadIdx.x; j < e; j += kNormBlock) one(j);
+}
+
+// Tensor that chunk c belongs to: the last one whose first chunk is <= c.
+template <int N> __device__ __forceinline__ int find(const Entries<N>& l, unsigned c) {
+    int lo = 0, hi = l.count;
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (l.e[mid].first <= c) lo = mid;
+        else hi = mid;
+    }
+    return lo;
+}
+
+template <typename T, bool INF>
+__device__ __forceinline__ void norm_chunk(const T* g, long long b, long long e, double& sum, unsigned& top) {
+    walk(
+        g, b, e,
+        [&](long long i) {
+            const float f[1] = {(float)g[i]};
+            if (INF) top = max(top, __float_as_uint(fabsf(f[0])));
+            else sum += square_sum(f);
+        },
+        [&](long long, uint4 w) {
+            float f[Vec16<T>::n];
+            Vec16<T>::unpack(w, f);
+            if (INF) {
+                // magnitudes order like their bits, with NaN above infinity
+#pragma unroll
+                for (int k = 0; k < Vec16<T>::n; ++k) top = max(top, __float_as_uint(fabsf(f[k])));
+            } else {
+                sum += square_sum(f);
+            }
+        });
+}
+
+// grid: blocks [part0, part0 + gridDim.x) of the call's partials; `finish` =
+// number of partials of the call when this is its last launch, else 0.
+template <int N, bool INF>
+__global__ void __launch_bounds__(kNormBlock)
+k_grad_norm(const __grid_constant__ Entries<N> l, NormScratch* ws, int part0, int finish, float* norm) {
+    __shared__ double red[kNormBlock / 32];
+    __shared__ bool last;
+    const int tid = threadIdx.x;
+    double sum = 0.0;
+    unsigned top = 0;
+    for (unsigned c = blockIdx.x; c < l.chunks; c += gridDim.x) {
+        const Entry& t = l.e[find(l, c)];
+        const long long b = (long long)(c - t.first) * kChunk;
+        const long long e = min(b + kChunk, t.numel);
+        if (t.dtype == GS_F32) norm_chunk<float, INF>(static_cast<const float*>(t.src), b, e, sum, top);
+        else if (t.dtype == GS_BF16)
+            norm_chunk<__nv_bfloat16, INF>(static_cast<const __nv_bfloat16*>(t.src), b, e, sum, top);
+        else norm_chunk<__half, INF>(static_cast<const __half*>(t.src), b, e, sum, top);
+    }
+    auto block_join = [&](double v) {
+        for (int d = 16; d; d >>= 1) {
+            const double o = __shfl_down_sync(~0u, v, d);
+            v = INF ? (o > v ? o : v) : v + o;
+        }
+        if ((tid & 31) == 0) red[tid >> 5] = v;
+        __syncthreads();
+        if (tid == 0)
+            for (int w = 1; w < kNormBlock / 32; ++w) v = INF ? (red[w] > v ? red[w] : v) : v + red[w];
+        return v;  // thread 0
+    };
+    // magnitudes travel as their bits, exact in a double
+    const double mine = block_join(INF ? (double)top : sum);
+    if (tid == 0) {
+        ws->part[part0 + blockIdx.x] = mine;
+        __threadfence();
+        last = finish && atomicAdd(&ws->ticket, 1u) == gridDim.x - 1;
+    }
+    __syncthreads();
+    if (!last) return;
+    __threadfence();
+    double v = 0.0;
+    for (int i = tid; i < finish; i += kNormBlock) {
+        const double o = __ldcg(&ws->part[i]);
+        v = INF ? (o > v ? o : v) : v + o;
+    }
+    v = block_join(v);
+    if (tid == 0) {
+        *norm = INF ? __uint_as_float((unsigned)v) : (float)sqrt(v);
+        ws->ticket = 0;
+    }
+}
+
+template <typename T>
+__device__ __forceinline__ void clip_chunk(const T* g, T* o, long long b, long long e, float coef) {
+    if ((((uintptr_t)g ^ (uintptr_t)o) & 15) == 0) {
+        walk(
+            g, b, e, [&](long long i) { o[i] = (T)((float)g[i] * coef); },
+            [&](long long i, uint4 w) {
+                float f[Vec16<T>::n];
+                Vec16<T>::unpack(w, f);
+#pragma unroll
+                for (int k = 0; k < Vec16<T>::n; ++k) f[k] *= coef;
+                *reinterpret_cast<uint4*>(o + i) = Vec16<T>::pack(f);
+            });
+    } else {
+        for (long long i = b + threadIdx.x; i < e; i += kNormBlock) o[i] = (T)((float)g[i] * coef);
+    }
+}
+
+template <int N>
+__global__ void __launch_bounds__(kNormBlock)
+k_grad_clip(const __grid_constant__ Entries<N> l, const float* norm, float max_norm, float eps) {
+    const float q = max_norm / (*norm + eps);
+    const float coef = q > 1.0f ? 1.0f : q;  // a NaN stays
+    for (unsigned c = blockIdx.x; c < l.chunks; c += gridDim.x) {
+        const Entry& t = l.e[find(l, c)];
+        if (coef == 1.0f && t.src == t.dst) continue;
+        const long long b = (long long)(c - t.first) * kChunk;
+        const long long e = min(b + kChunk, t.numel);
+        if (t.dtype == GS_F32) clip_chunk(static_cast<const float*>(t.src), static_cast<float*>(t.dst), b, e, coef);
+        else if (t.dtype == GS_BF16)
+            clip_chunk(static_cast<const __nv_bfloat16*>(t.src), static_cast<__nv_bfloat16*>(t.dst), b, e, coef);
+        else clip_chunk(static_cast<const __half*>(t.src), static_cast<__half*>(t.dst), b, e, coef);
+    }
+}
+
+bool list_ok(const gs_tensor_list* l, void* const* dst, bool clip) {
+    if (!l || l->count < 0 || (l->count > 0 && (!l->data || !l->numel || !l->dtype))) return false;
+    for (int i = 0; i < l->count; ++i) {
+        const int d = l->dtype[i];
+        if (d != GS_F32 && d != GS_BF16 && d != GS_F16) return false;
+        if (l->numel[i] < 0 || l->numel[i] > (1ll << 40)) return false;
+        if (l->numel[i] == 0) continue;
+        const size_t es = d == GS_F32 ? 4 : 2;
+        if (!l->data[i] || !aligned(l->data[i], es)) return false;
+        if (clip && dst && (!dst[i] || !aligned(dst[i], es))) return false;
+    }
+    return true;
+}
+
+// Next entries of the list from position i on (empty tensors left out).
+template <int N> int fill(const gs_tensor_list* l, void* const* dst, int i, Entries<N>* out) {
+    out->count = 0;
+    unsigned long long chunks = 0;
+    for (; i < l->count && out->count < N; ++i) {
+        if (l->numel[i] == 0) continue;
+        const unsigned long long n = (unsigned long long)((l->numel[i] + kChunk - 1) / kChunk);
+        if (chunks + n > 0x7fffffffull && out->count) break;
+        Entry& e = out->e[out->count++];
+        e.src = l->data[i];
+        e.dst = dst ? dst[i] : const_cast<void*>(l->data[i]);
+        e.numel = l->numel[i];
+        e.first = (unsigned)chunks;
+        e.dtype = l->dtype[i];
+        chunks += n;
+    }
+    out->chunks = (unsigned)chunks;
+    return i;
+}
+
+template <int N>
+int norm_launches(const gs_tensor_list* l, int kind, float* norm, NormScratch* ws, cudaStream_t s) {
+    static thread_local Entries<N> e;
+    // the call's partials are shared out evenly over its launches
+    int launches = 0;
+    for (int i = 0; i < l->count;) {
+        i = fill(l, nullptr, i, &e);
+        launches += e.count > 0;
+    }
+    if (launches > kMaxGrid) return GS_ERR_INVALID_ARG;
+    const int share = launches ? kMaxGrid / launches : 1;
+    int part = 0, done = 0, i = 0;
+    do {
+        i = fill(l, nullptr, i, &e);
+        if (e.count == 0 && launches > 0) continue;
+        ++done;
+        unsigned grid = e.chunks < (unsigned)share ? e.chunks : (unsigned)share;
+        if (grid == 0) grid = 1;
+        const int finish = done >= launches ? part + (int)grid : 0;
+        auto k = kind == GS_NORM_INF ? k_grad_norm<N, true> : k_grad_norm<N, false>;
+        k<<<grid, kNormBlock, 0, s>>>(e, ws, part, finish, norm); note_launch();
+        GS_LAUNCH_CHECK();
+        part += (int)grid;
+    } while (i < l->count);
+    return GS_OK;
+}
+
+template <int N>
+int clip_launches(const gs_tensor_list* l, void* const* dst, const float* norm, float max_norm, float eps,
+                  cudaStream_t s) {
+    static thread_local Entries<N> e;
+    for (int i = 0; i < l->count;) {
+        i = fill(l, dst, i, &e);
+        if (e.count == 0) continue;
+        const unsigned grid = e.chunks < (unsigned)kMaxGrid ? e.chunks : (unsigned)kMaxGrid;
+        k_grad_clip<N><<<grid, kNormBlock, 0, s>>>(e, norm, max_norm, eps); note_launch();
+        GS_LAUNCH_CHECK();
+    }
+    return GS_OK;
+}
+
+}  // namespace
+}  // namespace gs
+
+using namespace gs;
+
+extern "C" size_t gs_grad_norm_workspace_bytes(void) { return sizeof(NormScratch); }
+
+extern "C" int gs_grad_norm(const gs_tensor_list* list, int kind, float* norm, void* ws, size_t ws_bytes,
+                            void* stream) {
+    if (!list_ok(list, nullptr, false) || (kind != GS_NORM_L2 && kind != GS_NORM_INF)) return GS_ERR_INVALID_ARG;
+    if (!norm || !aligned(norm, 4) || !ws || ws_bytes < sizeof(NormScratch) || !aligned(ws, 16))
+        return GS_ERR_INVALID_ARG;
+    NormScratch* w = static_cast<NormScratch*>(ws);
+    cudaStream_t s = (cudaStream_t)stream;
+    return list->count <= kSmallList ? norm_launches<kSmallList>(list, kind, norm, w, s)
+                                     : norm_launches<kLargeList>(list, kind, norm, w, s);
+}
+
+extern "C" int gs_grad_clip(const gs_tensor_list* list, void* const* dst, const float* norm, float max_norm, float eps,
+                            void* stream) {
+    if (!list_ok(list, dst, true) || !norm || !aligned(norm, 4) || !(max_norm >= 0.0f) || !(eps >= 0.0f))
+        return GS_ERR_INVALID_ARG;
+    cudaStream_t s = (cudaStream_t)stream;
+    return list->count <= kSmallList ? clip_launches<kSmallList>(list, dst, norm, max_norm, eps, s)
+                                     : clip_launches<kLargeList>(list, dst, norm, max_norm, eps, s);
+}

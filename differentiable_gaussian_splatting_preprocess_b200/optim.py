@@ -1,0 +1,80 @@
+"""Gradient norm and clipping between the backward stages and the optimiser
+step (``binding.gs_adam_step``).  A ``GradList`` names the gradient tensors
+once; the norm and the clipping then run over all of them in one launch each.
+
+    grads = optim.GradList([g["dL_dmeans"], g["dL_dscales"], ...])
+    norm = optim.clip_grads(grads, max_norm=1.0)        # in place, or out=...
+or, with the scaling folded into the optimiser's read of the gradients:
+    norm = optim.grad_norm(grads)
+    binding.gs_adam_step_clipped(cfg, step, params, g, m, v, norm, 1.0)
+"""
+from __future__ import annotations
+
+from typing import Optional, Sequence
+
+import torch
+
+from . import binding as B
+
+_KINDS = {"l2": B.GS_NORM_L2, "inf": B.GS_NORM_INF}
+
+
+class GradList:
+    """Contiguous CUDA tensors of one device (float32, bfloat16 or float16 in
+    any mixture) and the workspace of their norm.  Holds the tensors: make a
+    new list when they are replaced by others.  Norms of one list must not
+    overlap on the GPU (they share its workspace)."""
+
+    def __init__(self, tensors: Sequence[torch.Tensor]):
+        self.tensors = [t.detach() for t in tensors]
+        if not self.tensors:
+            raise ValueError("a GradList needs at least one tensor")
+        self.c, self.data = B.tensor_list(self.tensors)
+        self.device = self.tensors[0].device
+        self.ws = torch.zeros(B.gs_grad_norm_workspace_bytes(), dtype=torch.uint8, device=self.device)
+        self._writable = None  # destination this list was last checked against
+
+    def _check_out(self, out: "GradList") -> None:
+        if self._writable is out:
+            return
+        if len(out.tensors) != len(self.tensors):
+            raise ValueError(f"out has {len(out.tensors)} tensors, the list has {len(self.tensors)}")
+        for i, (t, o) in enumerate(zip(self.tensors, out.tensors)):
+            if t.shape != o.shape or t.dtype != o.dtype or t.device != o.device:
+                raise ValueError(f"out[{i}] must be {t.dtype} of shape {tuple(t.shape)} on {t.device}")
+        span = lambda t: (t.data_ptr(), t.data_ptr() + t.numel() * t.element_size())  # noqa: E731
+        spans = [(*span(o), True, i) for i, o in enumerate(out.tensors) if o.numel()]
+        # sources that are scaled in place are their destination's span
+        spans += [(*span(t), False, i) for i, (t, o) in enumerate(zip(self.tensors, out.tensors))
+                  if t.numel() and t.data_ptr() != o.data_ptr()]
+        reach = {False: (0, 0), True: (0, 0)}  # furthest end (and tensor) of the ranges read, written so far
+        for beg, end, written, i in sorted(spans):
+            for kind in (False, True):
+                if (kind or written) and reach[kind][0] > beg:
+                    raise ValueError(f"out[{i if written else reach[kind][1]}] overlaps another tensor of the lists")
+            reach[written] = max(reach[written], (end, i))
+        self._writable = out
+
+
+def grad_norm(grads: GradList, kind: str = "l2", out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """Norm over all elements of all tensors, float32 [1] on the device:
+    sqrt(sum g^2) ("l2") or max |g| ("inf")."""
+    if kind not in _KINDS:
+        raise ValueError(f"kind must be one of {sorted(_KINDS)}, got {kind!r}")
+    if out is None:
+        with torch.cuda.stream(stream):  # None: the current stream
+            out = torch.empty(1, dtype=torch.float32, device=grads.device)
+    norm = out
+    B._same_device(grads.ws, (norm,))
+    B.gs_grad_norm(grads.c, norm, grads.ws, _KINDS[kind], stream)
+    return norm
+
+
+def clip_grads(grads: GradList, max_norm: float, out: Optional[GradList] = None, kind: str = "l2", eps: float = 1e-6,
+               stream=None) -> torch.Tensor:
+    """Scales the gradients by min(1, max_norm / (norm + eps)), in place or
+    into the tensors of ``out``; returns the norm before scaling."""
+    grads._check_out(grads if out is None else out)
+    norm = grad_norm(grads, kind, None, stream)
+    B.gs_grad_clip(grads.c, norm, max_norm, None if out is None else out.data, eps, stream)
+    return norm

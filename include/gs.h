@@ -385,6 +385,154 @@ GS_API int gs_adam_step(const gs_adam_config* cfg, int step, int N, int C, float
                         const float* dL_dscales, const float* dL_dquats, const float* dL_dopacity,
                         const float* dL_dcolors, float* m, float* v, float* scales, float* opacity, void* stream);
 
+/*
+ * Gated linear recurrence ([CB] 2: the compositing recurrence
+ * S <- (1 - a) S + a c over given samples, with any number of channels; used
+ * by itself for ray samples and for per-sequence state).
+ *
+ *   h_t = a_t h_{t-1} + u_t,   u_t = x_t, or (1 - a_t) x_t with
+ *   GS_SCAN_COUPLED, along every sequence; h before a sequence's first row
+ *   is h0 of that sequence (0 when h0 is NULL).
+ *
+ * Layout: `rows` rows in all; x and h have `channels` channels a row, a has
+ *   `gates` gates a row, channel c using gate c / (channels / gates) (gates
+ *   divides channels: one gate per channel, per head of channels, or for the
+ *   whole row).  Elements of a row are contiguous; stride_* are the elements
+ *   between the starts of neighbouring rows (>= channels or gates).
+ * Sequences: seq_offsets [n_seq + 1] int64 (device), increasing, sequence s
+ *   being rows [seq_offsets[s], seq_offsets[s + 1]); lengths of 0 are valid
+ *   (h_last = h0, dL_dh0 = dL_dh_last).  Rows in front of seq_offsets[0] and
+ *   from seq_offsets[n_seq] on belong to no sequence: outputs leave them as
+ *   they were, or write zeros with GS_SCAN_ZERO_PAD.  seq_offsets = NULL:
+ *   n_seq sequences of rows / n_seq rows each (n_seq must divide rows).
+ *   Offsets out of range or not increasing give unspecified values, but no
+ *   access outside the arguments.
+ * GS_SCAN_REVERSE runs every sequence from its last row to its first (the
+ *   back-to-front order of samples listed front to back); "before" and
+ *   "last" above are then meant in that order.
+ * Types: x, h and their gradients are `dtype` (GS_F32, GS_BF16, GS_F16); a
+ *   and its gradient are gate_dtype (GS_F32 or dtype); h0, h_last, states
+ *   and their gradients are fp32.  States, gate products and gradients are
+ *   held in fp32 and each output is rounded once.  Gates are meant to lie in
+ *   [-1, 1]: products of gates over many rows are formed, so where they leave
+ *   fp32's range and meet a state other than 0 the result is not finite.
+ * Outputs must not overlap inputs or one another.
+ */
+#define GS_F32 0
+#define GS_BF16 1
+#define GS_F16 2
+
+#define GS_SCAN_REVERSE 1
+#define GS_SCAN_COUPLED 2
+#define GS_SCAN_ZERO_PAD 4
+
+typedef struct gs_scan_desc {
+    long long rows;                         /* of all sequences together */
+    int channels, gates;
+    int n_seq;
+    int dtype, gate_dtype;
+    int flags;
+    long long stride_a, stride_x, stride_h; /* elements between rows */
+    long long stride_da, stride_dx, stride_dh;
+} gs_scan_desc;
+
+/* Bytes of workspace the two scans of this description need (0: none, or an
+ * invalid description).  A workspace must be zero-filled once before its
+ * first use; every call leaves it ready for the next, of any description
+ * that fits.  Calls that may overlap on the GPU need a workspace each. */
+GS_API size_t gs_scan_workspace_bytes(const gs_scan_desc* desc);
+
+/* Bytes of `states`, the forward's record for gs_scan_bwd. */
+GS_API size_t gs_scan_states_bytes(const gs_scan_desc* desc);
+
+/*
+ * gs_scan_fwd - writes h [rows, channels] (NULL to skip: the last state
+ *   only), h_last [n_seq, channels] (NULL to skip) and states (NULL when no
+ *   backward follows): the state in front of every chunk of rows.
+ * ws: >= gs_scan_workspace_bytes(desc) bytes, 16-byte aligned (may be NULL
+ *   when that is 0).  A wait between chunks that runs out raises
+ *   GS_ERR_TIMEOUT in its status word; the outputs are then incomplete.
+ */
+GS_API int gs_scan_fwd(const gs_scan_desc* desc, const void* a, const void* x, const float* h0,
+                       const long long* seq_offsets, void* h, float* h_last, float* states, void* ws,
+                       size_t ws_bytes, void* stream);
+
+/*
+ * gs_scan_bwd - the gradients of gs_scan_fwd's inputs from those of its
+ *   outputs, dL_dh [rows, channels] and dL_dh_last [n_seq, channels] (each
+ *   may be NULL: zero):  g_t = dL_dh_t + a_{t+1} g_{t+1} (+ dL_dh_last at a
+ *   sequence's last row); dL_da = sum over the gate's channels of
+ *   g_t (h_{t-1} - [coupled] x_t); dL_dx = g_t (coupled: (1 - a_t) g_t);
+ *   dL_dh0 [n_seq, channels] (NULL to skip) = a g at the first row.
+ * The states h_{t-1} are recomputed in fp32 from a, x, h0 and `states`, so h
+ *   itself is not needed.  desc, a, x, h0 and seq_offsets as in the forward
+ *   (same strides of a and x).  Outputs are OVERWRITTEN.  Sums run in a
+ *   fixed order: equal inputs give equal bits.
+ */
+GS_API int gs_scan_bwd(const gs_scan_desc* desc, const void* a, const void* x, const float* h0,
+                       const long long* seq_offsets, const float* states, const void* dL_dh,
+                       const float* dL_dh_last, void* dL_da, void* dL_dx, float* dL_dh0, void* ws,
+                       size_t ws_bytes, void* stream);
+
+/*
+ * gs_scan_step - one row of the recurrence for each of `rows` kept states
+ *   (n_seq = rows; the form for single tokens): state_out = a state + u, and
+ *   h = state_out in `dtype` (NULL to skip).  state, state_out [rows,
+ *   channels] fp32, dense; state_out may be `state`.
+ */
+GS_API int gs_scan_step(const gs_scan_desc* desc, const void* a, const void* x, const float* state,
+                        float* state_out, void* h, void* stream);
+
+/*
+ * Gradient norm and clipping over a list of tensors ([CR]'s stability notes
+ * list gradient clipping; the stage between the backward and gs_adam_step).
+ *
+ * gs_tensor_list (host arrays, read during the call): `count` tensors,
+ *   data[i] (device) of numel[i] contiguous elements of type dtype[i]
+ *   (GS_F32, GS_BF16 or GS_F16).  Tensors may be empty (data NULL allowed).
+ *
+ * gs_grad_norm - *norm (fp32) = sqrt(sum g^2) over all elements of all
+ *   tensors (GS_NORM_L2), or max |g| (GS_NORM_INF).  The sum is held in 64
+ *   bits and squares neither overflow nor vanish in between; the order of
+ *   the sum is fixed, so equal inputs give equal bits.  A NaN anywhere gives
+ *   NaN; an empty list gives 0.
+ *   ws: >= gs_grad_norm_workspace_bytes() bytes, 16-byte aligned,
+ *   zero-filled once before its first use.
+ * gs_grad_clip - dst[i] = g min(1, max_norm / (*norm + eps)), computed in
+ *   fp32 and rounded once to dtype[i].  dst: host array of device pointers,
+ *   or NULL to scale the tensors in place; a dst[i] may be data[i], and must
+ *   not overlap any tensor otherwise.  A NaN norm makes every element NaN,
+ *   an infinite one makes finite elements 0.  max_norm >= 0, eps >= 0.
+ */
+#define GS_NORM_L2 0
+#define GS_NORM_INF 1
+
+typedef struct gs_tensor_list {
+    int count;
+    const void* const* data;
+    const long long* numel;
+    const int* dtype;
+} gs_tensor_list;
+
+GS_API size_t gs_grad_norm_workspace_bytes(void);
+GS_API int gs_grad_norm(const gs_tensor_list* list, int kind, float* norm, void* ws, size_t ws_bytes, void* stream);
+GS_API int gs_grad_clip(const gs_tensor_list* list, void* const* dst, const float* norm, float max_norm, float eps,
+                        void* stream);
+
+/*
+ * gs_adam_step_clipped - gs_adam_step on the gradients scaled by
+ *   min(1, max_norm / (*grad_norm + clip_eps)): the clipping pass folded
+ *   into the optimiser's read of the gradients.  grad_norm: one fp32 on the
+ *   device, e.g. gs_grad_norm over the five gradient tensors (so the norm is
+ *   that of the gradients w.r.t. the activated values).  Everything else as
+ *   gs_adam_step.
+ */
+GS_API int gs_adam_step_clipped(const gs_adam_config* cfg, int step, int N, int C, float* means, float* log_scales,
+                                float* quats, float* logit_opacity, float* colors, const float* dL_dmeans,
+                                const float* dL_dscales, const float* dL_dquats, const float* dL_dopacity,
+                                const float* dL_dcolors, float* m, float* v, float* scales, float* opacity,
+                                const float* grad_norm, float max_norm, float clip_eps, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -1,0 +1,282 @@
+"""Gradient norm, clipping and the clipped Adam step against float64.
+
+Tolerances.  The sum of squares: each block's fp32 sums run over at most 8
+squares (9 roundings), the rest is 64-bit, so the sum is within 9 u (u =
+2^-24) and its root, rounded once more, within 5 u + u = 6 u.  The clipping
+factor adds the sum with eps, the division and the factor's own product: 4 u
+more; then half a step of the tensor's type."""
+import numpy as np
+import pytest
+import torch
+
+from oracle import adam as A
+from differentiable_gaussian_splatting_preprocess_b200 import autograd as GA
+from differentiable_gaussian_splatting_preprocess_b200 import binding as B
+from differentiable_gaussian_splatting_preprocess_b200 import optim
+
+pytestmark = pytest.mark.gpu
+
+U = 2.0 ** -24
+DTS = [torch.float32, torch.bfloat16, torch.float16]
+
+
+def _norm64(ts):
+    return float(np.sqrt(sum(float((t.double() ** 2).sum()) for t in ts)))
+
+
+def _tensors(seed, sizes, dts=DTS, scale=1.0):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    return [(scale * torch.randn(n, generator=g, device="cuda")).to(dts[i % len(dts)]) for i, n in enumerate(sizes)]
+
+
+SIZES = [[1], [7], [4096], [16384], [16385], [0, 5, 0], [100001, 3, 1, 50000], [33] * 33, [2000] * 1000,
+         [1 << 22], [999] * 2500]
+
+
+@pytest.mark.parametrize("sizes", SIZES, ids=lambda s: f"{len(s)}x{s[0]}")
+def test_norm_and_clip(sizes):
+    ts = _tensors(len(sizes) + sizes[0], sizes)
+    want = _norm64(ts)
+    lst = optim.GradList(ts)
+    norm = optim.grad_norm(lst)
+    assert abs(float(norm) - want) <= 6 * U * want
+    top = max((float(t.float().abs().max()) for t in ts if t.numel()), default=0.0)
+    assert float(optim.grad_norm(lst, "inf")) == top
+    keep = [t.clone() for t in ts]
+    for max_norm in (0.3 * want, 3.0 * want + 1e-3):
+        c = min(1.0, float(np.float32(max_norm)) / (want + float(np.float32(1e-6))))
+        out = optim.GradList([torch.full_like(t, 9.0) for t in ts])
+        assert torch.equal(optim.clip_grads(lst, max_norm, out=out), norm)
+        for t, o in zip(ts, out.tensors):
+            w = t.double() * c
+            tiny = 2.0 ** -25 if t.dtype == torch.float16 else 0.0
+            assert ((o.double() - w).abs() <= (10 * U + torch.finfo(t.dtype).eps / 2) * w.abs() + tiny).all()
+        inplace = optim.GradList([t.clone() for t in ts])
+        optim.clip_grads(inplace, max_norm)
+        for p, q in zip(inplace.tensors, out.tensors):
+            assert torch.equal(p, q)
+    for t, k in zip(ts, keep):
+        assert torch.equal(t, k)
+
+
+@pytest.mark.parametrize("dtype", DTS)
+@pytest.mark.parametrize("shift", [1, 2, 3, 5])
+def test_unaligned_tensors(dtype, shift):
+    base = _tensors(shift, [40000], [dtype])[0]
+    dst = torch.full((40020,), 9.0, dtype=dtype, device="cuda")
+    src = base[shift:shift + 33333]
+    for at in (shift, shift + 1):
+        dst.fill_(9.0)
+        out = dst[at:at + 33333]
+        norm = optim.clip_grads(optim.GradList([src]), 1.0, out=optim.GradList([out]))
+        assert abs(float(norm) - _norm64([src])) <= 6 * U * _norm64([src])
+        want = torch.empty_like(src)
+        optim.clip_grads(optim.GradList([src.clone()]), 1.0, out=optim.GradList([want]))
+        assert torch.equal(out, want)
+        assert (dst[:at] == 9).all() and (dst[at + 33333:] == 9).all()
+
+
+@pytest.mark.parametrize("scale", [1e-30, 1e-22, 1e-15, 1e15, 1e22, 1e30])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_squares_neither_overflow_nor_vanish(scale, dtype):
+    ts = _tensors(4, [5000, 77], [dtype], scale)
+    want = _norm64(ts)
+    assert abs(float(optim.grad_norm(optim.GradList(ts))) - want) <= 6 * U * want
+    mixed = ts + _tensors(5, [300], [dtype], 1.0)
+    want = _norm64(mixed)
+    assert abs(float(optim.grad_norm(optim.GradList(mixed))) - want) <= 6 * U * want
+
+
+def test_zero_infinite_and_nan_gradients():
+    z = [torch.zeros(1000, device="cuda"), torch.zeros(3, dtype=torch.bfloat16, device="cuda")]
+    lst = optim.GradList(z)
+    assert float(optim.clip_grads(lst, 1.0)) == 0.0 and all((t == 0).all() for t in z)
+    for kind in ("l2", "inf"):
+        for bad in (float("inf"), float("-inf"), float("nan")):
+            t = torch.ones(70000, device="cuda")
+            t[65000] = bad
+            n = float(optim.grad_norm(optim.GradList([t, z[0]]), kind))
+            assert (n != n) if bad != bad else n == float("inf")
+    t = torch.ones(100, device="cuda")
+    t[3] = float("inf")
+    optim.clip_grads(optim.GradList([t]), 1.0)
+    assert t[3].isnan() and (torch.cat([t[:3], t[4:]]) == 0).all()  # as g * (max_norm / inf) is
+    t = torch.ones(100, device="cuda")
+    t[3] = float("nan")
+    optim.clip_grads(optim.GradList([t]), 1.0)
+    assert t.isnan().all()
+    one = torch.ones(5, device="cuda")
+    optim.clip_grads(optim.GradList([one]), 0.0)
+    assert (one == 0).all()
+
+
+def test_equal_bits_streams_and_capture():
+    ts = _tensors(3, [300000, 5, 70001, 12, 1 << 20])
+    lst = optim.GradList(ts)
+    want = optim.grad_norm(lst).clone()
+    for _ in range(5):
+        assert torch.equal(optim.grad_norm(lst), want)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    other = optim.GradList(ts)
+    n2 = optim.grad_norm(other, stream=side)
+    side.synchronize()
+    assert torch.equal(n2, want)
+    out = optim.GradList([torch.empty_like(t) for t in ts])
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        norm = optim.clip_grads(lst, 1.0, out=out)
+    for seed in (8, 9):
+        for t, v in zip(ts, _tensors(seed, [t.numel() for t in ts])):
+            t.copy_(v)
+        g.replay()
+        eager = optim.GradList([torch.empty_like(t) for t in ts])
+        assert torch.equal(norm, optim.clip_grads(lst, 1.0, out=eager))
+        for p, q in zip(out.tensors, eager.tensors):
+            assert torch.equal(p, q)
+
+
+def test_refusals():
+    t = torch.ones(10, device="cuda")
+    with pytest.raises(ValueError):
+        optim.GradList([])
+    with pytest.raises(ValueError):
+        optim.GradList([t.double()])
+    with pytest.raises(ValueError):
+        optim.GradList([t.cpu()])
+    with pytest.raises(ValueError):
+        optim.GradList([torch.ones(4, 4, device="cuda").t()[1:]])
+    with pytest.raises(ValueError):
+        optim.grad_norm(optim.GradList([t]), "l1")
+    with pytest.raises(ValueError):
+        optim.clip_grads(optim.GradList([t, t]), 1.0)                       # scaled twice
+    with pytest.raises(ValueError):
+        optim.clip_grads(optim.GradList([t[:6], t[5:]]), 1.0)
+    with pytest.raises(ValueError):
+        optim.clip_grads(optim.GradList([t]), 1.0, out=optim.GradList([t[:9]]))
+    big = torch.ones(30, device="cuda")
+    with pytest.raises(ValueError):  # a destination inside another tensor's source
+        optim.clip_grads(optim.GradList([big[:10], big[10:20]]), 1.0, out=optim.GradList([big[15:25], big[:10]]))
+    with pytest.raises(B.GsError):
+        optim.clip_grads(optim.GradList([t]), -1.0)
+    optim.clip_grads(optim.GradList([big[:10], big[10:20]]), 1.0, out=optim.GradList([big[:10], big[20:]]))
+
+
+def _adam_state(seed, n, c):
+    rng = np.random.default_rng(seed)
+    q = rng.normal(size=(n, 4))
+    q /= np.linalg.norm(q, axis=1, keepdims=True)
+    cu = lambda v: torch.from_numpy(np.asarray(v, np.float32)).cuda()  # noqa: E731
+    p = dict(means=cu(rng.normal(size=(n, 3))), log_scales=cu(rng.normal(-4, 0.5, size=(n, 3))), quats=cu(q),
+             logit_opacity=cu(rng.normal(size=n)), colors=cu(rng.uniform(size=(n, c))))
+    g = dict(dL_dmeans=cu(rng.normal(size=(n, 3))), dL_dscales=cu(50 * rng.normal(size=(n, 3))),
+             dL_dquats=cu(rng.normal(size=(n, 4))), dL_dopacity=cu(rng.normal(size=n)),
+             dL_dcolors=cu(rng.normal(size=(n, c))))
+    m = cu(0.1 * rng.normal(size=(11 + c) * n))
+    v = cu(0.01 * rng.uniform(size=(11 + c) * n) + 1e-4)
+    return p, g, m, v
+
+
+CFG = B.GsAdamConfig(1.6e-4, 5e-3, 1e-3, 5e-2, 2.5e-3, 0.9, 0.999, 1e-15, 10)
+
+
+@pytest.mark.parametrize("n,c", [(1, 3), (5, 0), (1000, 3), (3001, 48), (4096, 12)])
+def test_clipped_adam_is_adam_on_clipped_gradients(n, c):
+    """Bit for bit: the factor is applied to each gradient in fp32 in both."""
+    p, g, m, v = _adam_state(n + c, n, c)
+    p2, m2, v2 = {k: t.clone() for k, t in p.items()}, m.clone(), v.clone()
+    for max_norm in (1.0, 1e9):
+        clipped = {k: t.clone() for k, t in g.items()}
+        norm = optim.clip_grads(optim.GradList(list(clipped.values())), max_norm)
+        s, o = torch.empty((n, 3), device="cuda"), torch.empty(n, device="cuda")
+        s2, o2 = torch.empty_like(s), torch.empty_like(o)
+        B.gs_adam_step(CFG, 3, p, clipped, m, v, s, o)
+        B.gs_adam_step_clipped(CFG, 3, p2, g, m2, v2, norm, max_norm, s2, o2)
+        for k in p:
+            assert torch.equal(p[k], p2[k]), k
+        assert torch.equal(m, m2) and torch.equal(v, v2) and torch.equal(s, s2) and torch.equal(o, o2)
+
+
+def test_clipped_adam_matches_the_oracle():
+    n, c = 2000, 12
+    p, g, m, v = _adam_state(7, n, c)
+    to = lambda t: t.double().cpu().numpy()  # noqa: E731
+    before = {k: to(t) for k, t in p.items()}
+    sizes = dict(means=(n, 3), log_scales=(n, 3), quats=(n, 4), logit_opacity=(n,), colors=(n, c))
+
+    def split(flat):
+        out, off = {}, 0
+        for k in A.GROUPS:
+            cnt = int(np.prod(sizes[k]))
+            out[k] = to(flat)[off:off + cnt].reshape(sizes[k])
+            off += cnt
+        return out
+
+    m0, v0 = split(m), split(v)
+    norm64 = _norm64(g.values())
+    coef = min(1.0, 2.0 / (norm64 + 1e-6))
+    f = lambda x: float(np.float32(x))  # noqa: E731
+    lr = dict(means=f(1.6e-4), log_scales=f(5e-3), quats=f(1e-3), logit_opacity=f(5e-2), colors=f(2.5e-3))
+    want, wm, wv, _, _ = A.adam_step(before, {k: to(t) * coef for k, t in g.items()}, m0, v0, 3, lr, f(0.9), f(0.999),
+                                     f(1e-15), 10)
+    norm = optim.grad_norm(optim.GradList(list(g.values())))
+    B.gs_adam_step_clipped(CFG, 3, p, g, m, v, norm, 2.0)
+    gm, gv = split(m), split(v)
+    for k in A.GROUPS:
+        ulp = np.spacing(np.abs(want[k]).astype(np.float32)).astype(np.float64)
+        # as the unclipped step: a few ulps of the parameter and 1e-5 of the update
+        assert np.all(np.abs(to(p[k]) - want[k]) <= 8 * ulp + 1e-5 * np.abs(want[k] - before[k])), k
+        assert np.linalg.norm(gm[k] - wm[k]) <= 2e-6 * np.linalg.norm(wm[k]), k
+        assert np.linalg.norm(gv[k] - wv[k]) <= 1e-5 * np.linalg.norm(wv[k]), k
+
+
+def test_recurrence_norm_and_step_together():
+    """As a training step uses them: rays composited by the recurrence, its
+    gradients clipped together, one of them fed to Adam by way of the clipped
+    step's parameters; captured and replayed."""
+    rays, per, n = 200, 30, 6000
+    torch.manual_seed(0)
+    logit = torch.randn(n, 1, device="cuda", requires_grad=True)
+    color = torch.rand(n, 3, device="cuda", requires_grad=True)
+    off = torch.arange(0, n + 1, per, device="cuda")
+    target = torch.rand(rays, 3, device="cuda")
+    bg = torch.zeros(rays, 3, device="cuda")
+
+    def grads():
+        _, pix = GA.gated_scan(1 - torch.sigmoid(logit), color, h0=bg, seq_offsets=off, reverse=True, coupled=True,
+                               final_only=True)
+        return torch.autograd.grad(((pix - target) ** 2).sum(), [logit, color])
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        grads()
+    torch.cuda.current_stream().wait_stream(side)
+    p, g, m, v = _adam_state(1, n, 3)
+    p["colors"] = color.detach()
+    p["logit_opacity"] = logit.detach().view(n)
+    g_op, g_col = g["dL_dopacity"], g["dL_dcolors"]
+    ref = [t.clone() for t in grads()]
+    norm64 = _norm64(ref + [g[k] for k in ("dL_dmeans", "dL_dscales", "dL_dquats")])
+    lst = optim.GradList([g[k] for k in g])
+
+    def step():
+        gl, gc = grads()
+        g_op.copy_(gl.view(n)), g_col.copy_(gc)
+        norm = optim.grad_norm(lst)
+        B.gs_adam_step_clipped(CFG, 3, p, g, m, v, norm, 1.0)
+        return norm
+
+    graph = torch.cuda.CUDAGraph()
+    saved = [t.clone() for t in (*p.values(), m, v)]
+    with torch.cuda.graph(graph):
+        norm = step()
+    graph.replay()
+    torch.cuda.synchronize()
+    assert abs(float(norm) - norm64) <= 6 * U * norm64 * 2
+    got = [t.clone() for t in (*p.values(), m, v)]
+    for t, s in zip((*p.values(), m, v), saved):
+        t.data.copy_(s)
+    assert abs(float(step()) - norm64) <= 6 * U * norm64 * 2
+    for t, q in zip((*p.values(), m, v), got):
+        assert torch.equal(t, q)

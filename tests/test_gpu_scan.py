@@ -1,0 +1,450 @@
+"""The gated linear recurrence (gs_scan_fwd, gs_scan_bwd, gs_scan_step and
+their autograd interface) against its float64 oracle.
+
+Tolerances.  Every output is a sum of products of gates with one input, and
+the kernels evaluate it in fp32 in some order.  A term meets at most one
+rounding per multiplication and one per addition on its way: with L rows in
+the longest sequence, at most 2 L + 64 of them (64 covers the joins of runs,
+warps and chunks, the products 1 - a and x (1 - a), and the two products of a
+gradient), plus the number of channels that share a gate for its gradient.  So
+the error is at most gamma(n) = n u / (1 - n u), u = 2^-24, times the same sum
+with magnitudes (the oracle's `magnitude`), plus half a step of the output's
+type."""
+import numpy as np
+import pytest
+import torch
+
+from oracle import scan as O
+from differentiable_gaussian_splatting_preprocess_b200 import autograd as GA
+from differentiable_gaussian_splatting_preprocess_b200 import binding as B
+
+pytestmark = pytest.mark.gpu
+
+F32, BF16, F16 = torch.float32, torch.bfloat16, torch.float16
+U = 2.0 ** -24
+
+
+def _np(t):
+    return t.detach().double().cpu().numpy()
+
+
+def _offsets(lens, front=0):
+    return np.concatenate([[front], front + np.cumsum(lens)]).astype(np.int64)
+
+
+def _inputs(seed, T, C, G, S, xdt, adt, h0=True, neg=False):
+    g = torch.Generator().manual_seed(seed)
+    a = torch.sigmoid(3 + 1.5 * torch.randn(T, G, generator=g))
+    if neg:
+        a = a * torch.where(torch.rand(T, G, generator=g) < 0.5, -1.0, 1.0)
+    x = torch.randn(T, C, generator=g)
+    h = torch.randn(S, C, generator=g) if h0 else None
+    dh = torch.randn(T, C, generator=g)
+    dl = torch.randn(S, C, generator=g)
+    cu = lambda t, dt: None if t is None else t.to(dt).cuda()  # noqa: E731
+    return cu(a, adt), cu(x, xdt), cu(h, F32), cu(dh, xdt), cu(dl, F32)
+
+
+def _within(got, want, mag, n, dtype, what):
+    got, eps = _np(got), torch.finfo(dtype).eps / 2
+    gam = n * U / (1 - n * U)
+    tiny = 2.0 ** -24 if dtype == F16 else 1e-37  # below fp16's normal range steps are 2^-24
+    bound = gam * mag * (1 + eps) + eps * np.abs(want) + tiny
+    bad = ~(np.abs(got - want) <= bound)
+    assert not bad.any(), (what, int(bad.sum()), bad.size, np.argwhere(bad)[:4].tolist(),
+                           got[bad][:4], want[bad][:4], bound[bad][:4])
+
+
+def _check(a, x, h0, dh, dl, off, reverse, coupled, got, final_only=False):
+    """got: (h, h_last, da, dx, dh0) with None for what was not asked for."""
+    an, xn = _np(a), _np(x)
+    hn = None if h0 is None else _np(h0)
+    dhn = None if final_only else _np(dh)
+    L = int(np.diff(off).max()) if len(off) > 1 else 0
+    n = 2 * L + 64
+    per = x.shape[-1] // a.shape[-1]
+    h, last, before = O.forward(an, xn, off, hn, reverse, coupled)
+    hm, lastm, beforem = O.forward(an, xn, off, hn, reverse, coupled, magnitude=True)
+    grads = O.backward(an, xn, off, before, dhn, _np(dl), reverse, coupled)
+    gradm = O.backward(an, xn, off, beforem, dhn, _np(dl), reverse, coupled, magnitude=True)
+    if got[0] is not None:
+        _within(got[0], h, hm, n, x.dtype, "h")
+    _within(got[1], last, lastm, n, F32, "h_last")
+    if got[2] is not None:
+        _within(got[2], grads[0], gradm[0], 2 * n + per, a.dtype, "da")
+        _within(got[3], grads[1], gradm[1], n, x.dtype, "dx")
+    if got[4] is not None:
+        _within(got[4], grads[2], gradm[2], n, F32, "dh0")
+
+
+def _run(a, x, h0, dh, dl, off, reverse=False, coupled=False, final_only=False, workspace=None):
+    leaves = [t.clone().requires_grad_(True) if t is not None else None for t in (a, x, h0)]
+    h, last = GA.gated_scan(*leaves[:2], h0=leaves[2], seq_offsets=off, reverse=reverse, coupled=coupled,
+                            final_only=final_only, workspace=workspace)
+    outs, gs = ([last], [dl]) if final_only else ([h, last], [dh, dl])
+    grads = torch.autograd.grad(outs, [t for t in leaves if t is not None], gs)
+    return h, last, grads[0], grads[1], grads[2] if h0 is not None else None
+
+
+def _cuda_off(off):
+    return torch.from_numpy(off).cuda()
+
+
+# rows around the runs (17) and tiles of the different channel counts, one to
+# many chunks; channels from 1 to several blocks, odd and even
+SHAPES = [(1, 1), (2, 3), (17, 4), (18, 5), (300, 31), (135, 32), (136, 33), (137, 64), (273, 65), (1000, 128),
+          (4352, 1), (4353, 1), (9001, 2), (2500, 3), (1089, 4), (700, 96), (1500, 37)]
+
+
+@pytest.mark.parametrize("xdt,adt", [(F32, F32), (BF16, BF16), (BF16, F32), (F16, F16), (F16, F32)])
+@pytest.mark.parametrize("T,C", SHAPES)
+def test_one_sequence(T, C, xdt, adt):
+    a, x, h0, dh, dl = _inputs(T + C, T, C, C, 1, xdt, adt)
+    off = _offsets([T])
+    _check(a, x, h0, dh, dl, off, False, False, _run(a, x, h0, dh, dl, None))
+
+
+@pytest.mark.parametrize("reverse", [False, True])
+@pytest.mark.parametrize("coupled", [False, True])
+@pytest.mark.parametrize("xdt", [F32, BF16])
+@pytest.mark.parametrize("T,C,G", [(700, 3, 1), (700, 6, 2), (900, 64, 1), (900, 96, 1), (500, 192, 2), (500, 144, 3),
+                                   (400, 128, 8), (333, 130, 65), (260, 1, 1), (600, 20, 4), (300, 640, 10)])
+def test_shared_gates_ragged(T, C, G, xdt, reverse, coupled):
+    rng = np.random.default_rng(T + C)
+    cuts = np.sort(rng.integers(0, T + 1, 13))
+    off = np.concatenate([[0], cuts, cuts[-1:], [T]]).astype(np.int64)  # some empty
+    a, x, h0, dh, dl = _inputs(T + C, T, C, G, len(off) - 1, xdt, F32, neg=True)
+    _check(a, x, h0, dh, dl, off, reverse, coupled, _run(a, x, h0, dh, dl, _cuda_off(off), reverse, coupled))
+
+
+@pytest.mark.parametrize("reverse", [False, True])
+def test_ray_compositing_final_only(reverse):
+    rng = np.random.default_rng(1)
+    lens = rng.geometric(1 / 24, 3000) - 1
+    off = _offsets(lens)
+    T = int(off[-1])
+    a, x, h0, _, dl = _inputs(4, T, 3, 1, len(lens), F32, F32)
+    a = torch.where(torch.rand_like(a) < 0.3, torch.ones_like(a), a)  # empty space
+    a[::50] = 0.0                                                     # opaque samples
+    got = _run(a, x, h0, None, dl, _cuda_off(off), reverse, True, final_only=True)
+    assert got[0] is None
+    _check(a, x, h0, None, dl, off, reverse, True, got, final_only=True)
+
+
+@pytest.mark.parametrize("S,L,C,G", [(1, 1, 1, 1), (7, 1, 40, 40), (3, 137, 64, 64), (64, 5, 33, 11), (2, 3000, 4, 4),
+                                     (5, 1237, 33, 33)])
+def test_dense_batches(S, L, C, G):
+    a, x, h0, dh, dl = _inputs(S + L, S * L, C, G, S, F32, F32)
+    off = _offsets([L] * S)
+    a3, x3, dh3 = a.view(S, L, G), x.view(S, L, C), dh.view(S, L, C)
+    h, last, da, dx, dh0 = _run(a3, x3, h0, dh3, dl, None)
+    assert h.shape == x3.shape and da.shape == a3.shape
+    _check(a, x, h0, dh, dl, off, False, False, (h.view(-1, C), last, da.view(-1, G), dx.view(-1, C), dh0))
+
+
+@pytest.mark.parametrize("reverse", [False, True])
+@pytest.mark.parametrize("T,C,G", [(1500, 4, 1), (400, 64, 64), (300, 192, 2)])
+def test_rows_outside_the_sequences(T, C, G, reverse):
+    """NaN in rows of no sequence reaches nothing; the C entry points leave
+    those rows as they were, the autograd interface gives zeros."""
+    off = np.array([40, 40, 100, 230, T - 37], np.int64)
+    S = 4
+    a, x, h0, dh, dl = _inputs(9, T, C, G, S, F32, F32)
+    dead = torch.ones(T, dtype=torch.bool)
+    dead[40:T - 37] = False
+    for t in (a, x, dh):
+        t[dead.cuda()] = float("nan")
+    got = _run(a, x, h0, dh, dl, _cuda_off(off), reverse)
+    for t in (got[0], got[2], got[3]):
+        assert (t[dead.cuda()] == 0).all()
+    clean = [torch.nan_to_num(t) for t in (a, x, dh)]
+    live = slice(40, T - 37)
+    want = _run(clean[0], clean[1], h0, clean[2], dl, _cuda_off(off), reverse)
+    for k, (p, q) in enumerate(zip(got, want)):
+        assert torch.equal(p[live], q[live]) if k in (0, 2, 3) else torch.equal(p, q)
+    _check(clean[0], clean[1], h0, clean[2], dl, off, reverse, False, want)
+    # C entry points without GS_SCAN_ZERO_PAD
+    h, da, dx = torch.full_like(x, 7.0), torch.full_like(a, 7.0), torch.full_like(x, 7.0)
+    last, dh0 = torch.empty_like(h0), torch.empty_like(h0)
+    d = B.scan_desc(a, x, _cuda_off(off), reverse)
+    ws = torch.zeros(max(16, B.gs_scan_workspace_bytes(d)), dtype=torch.uint8, device="cuda")
+    states = torch.empty(B.gs_scan_states_bytes(d) // 4, device="cuda")
+    B.gs_scan_fwd(a, x, h, last, states, ws, h0, _cuda_off(off), reverse)
+    B.gs_scan_bwd(a, x, states, da, dx, dh, dl, dh0, ws, h0, _cuda_off(off), reverse)
+    for t, w in ((h, want[0]), (da, want[2]), (dx, want[3])):
+        assert (t[dead.cuda()] == 7.0).all()
+        assert torch.equal(t[live], w[live])
+    assert torch.equal(last, want[1]) and torch.equal(dh0, want[4])
+    assert B.gs_read_status(ws) == B.GS_OK
+
+
+def test_sequences_do_not_touch_one_another():
+    """Infinities and NaN of one sequence stay in it, gates of 0 included."""
+    C, lens = 5, [300, 700, 1, 900, 0, 400]
+    off = _offsets(lens)
+    T, S = int(off[-1]), len(lens)
+    a, x, h0, dh, dl = _inputs(2, T, C, C, S, F32, F32)
+    want = _run(a, x, h0, dh, dl, _cuda_off(off))
+    a2, x2, dh2, h02 = a.clone(), x.clone(), dh.clone(), h0.clone()
+    x2[off[1]:off[2]] = float("inf")
+    a2[off[3]:off[4]] = float("nan")
+    dh2[off[1]:off[2]] = float("-inf")
+    h02[3] = float("inf")
+    got = _run(a2, x2, h02, dh2, dl, _cuda_off(off))
+    for s in (0, 2, 4, 5):
+        r = slice(off[s], off[s + 1])
+        for k in (0, 2, 3):
+            assert torch.equal(got[k][r], want[k][r]), (s, k)
+        assert torch.equal(got[1][s], want[1][s]) and torch.equal(got[4][s], want[4][s])
+    assert got[0][off[3]:off[4]].isnan().all()
+
+
+def test_growing_and_vanishing_products():
+    """Gates whose product over a tile overflows fp32, with states that stay
+    finite because the inputs are zero up to the last rows; and gates of 0."""
+    T, C = 2000, 4
+    a = torch.full((T, C), 4.0, device="cuda")
+    a[:, 1] = 0.0
+    a[:, 2] = 1e-30
+    x = torch.zeros((T, C), device="cuda")
+    x[T - 5:] = 1.0
+    x[:, 1] = torch.randn(T, device="cuda")
+    h, last = GA.gated_scan(a, x)
+    off = _offsets([T])
+    want, wlast, _ = O.forward(_np(a), _np(x), off)
+    assert torch.isfinite(h).all()
+    np.testing.assert_allclose(_np(h), want, rtol=1e-6)
+    np.testing.assert_allclose(_np(last), wlast, rtol=1e-6)
+
+
+@pytest.mark.parametrize("xdt", [F32, BF16])
+@pytest.mark.parametrize("shift", [0, 1])
+def test_strided_and_unaligned_rows(xdt, shift):
+    """Gates and inputs as parts of one wider projection, at any element."""
+    T, C, G = 500, 72, 72
+    a, x, h0, dh, dl = _inputs(3, T, C, G, 1, xdt, xdt)
+    wide = torch.zeros((T, 3 * C + 8), dtype=xdt, device="cuda")
+    av, xv, dv = (wide[:, shift + i * C:shift + (i + 1) * C] for i in range(3))
+    av.copy_(a), xv.copy_(x), dv.copy_(dh)
+    want = _run(a, x, h0, dh, dl, None)
+    d = B.scan_desc(av, xv)
+    ws = torch.zeros(B.gs_scan_workspace_bytes(d), dtype=torch.uint8, device="cuda")
+    out = torch.full((T, 3 * C + 8), 5.0, dtype=xdt, device="cuda")
+    hv, dav, dxv = (out[:, shift + i * C:shift + (i + 1) * C] for i in range(3))
+    last, dh0 = torch.empty_like(h0), torch.empty_like(h0)
+    states = torch.empty(B.gs_scan_states_bytes(d) // 4, device="cuda")
+    B.gs_scan_fwd(av, xv, hv, last, states, ws, h0)
+    B.gs_scan_bwd(av, xv, states, dav, dxv, dv, dl, dh0, ws, h0)
+    for p, q in zip((hv, last, dav, dxv, dh0), want):
+        assert torch.equal(p, q)
+    assert (out[:, :shift] == 5).all() and (out[:, shift + 3 * C:] == 5).all()
+    # the autograd interface copies what it cannot address
+    h, _ = GA.gated_scan(a.t().contiguous().t(), x, h0)
+    assert torch.equal(h, want[0])
+
+
+def test_expanded_gradients_and_unused_outputs():
+    T, C = 400, 6
+    a, x, h0, _, _ = _inputs(3, T, C, 2, 1, F32, F32)
+    leaves = [t.clone().requires_grad_(True) for t in (a, x, h0)]
+    h, last = GA.gated_scan(leaves[0], leaves[1], leaves[2])
+    got = torch.autograd.grad(h.sum(), leaves)
+    want = _run(a, x, h0, torch.ones_like(x), torch.zeros_like(h0), None)
+    for p, q in zip(got, want[2:]):
+        assert torch.equal(p, q)
+    h, last = GA.gated_scan(leaves[0], leaves[1], leaves[2])
+    got = torch.autograd.grad(last.sum(), leaves)
+    want = _run(a, x, h0, torch.zeros_like(x), torch.ones_like(h0), None)
+    for p, q in zip(got, want[2:]):
+        assert torch.equal(p, q)
+
+
+def test_equal_inputs_give_equal_bits_and_workspaces_are_reused():
+    T, C, G = 6000, 192, 2
+    a, x, h0, dh, dl = _inputs(3, T, C, G, 1, BF16, F32)
+    ws = GA.scan_workspace(a, x)
+    want = _run(a, x, h0, dh, dl, None)
+    for _ in range(5):
+        for p, q in zip(_run(a, x, h0, dh, dl, None, workspace=ws), want):
+            assert torch.equal(p, q)
+    # a smaller call in the same workspace, then the first one again
+    b = _inputs(4, 900, 64, 64, 1, BF16, BF16)
+    small = _run(*b, None)
+    for p, q in zip(_run(*b, None, workspace=ws), small):
+        assert torch.equal(p, q)
+    for p, q in zip(_run(a, x, h0, dh, dl, None, workspace=ws), want):
+        assert torch.equal(p, q)
+    assert B.gs_read_status(ws) == B.GS_OK
+
+
+def test_captured_forward_and_backward_replay():
+    T, C = 3000, 48
+    a, x, h0, dh, dl = _inputs(5, T, C, C, 1, F32, F32)
+    leaves = [t.clone().requires_grad_(True) for t in (a, x, h0)]
+
+    def step():
+        h, last = GA.gated_scan(leaves[0], leaves[1], leaves[2])
+        return (h, last, *torch.autograd.grad([h, last], leaves, [dh, dl]))
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        for _ in range(2):
+            step()
+    torch.cuda.current_stream().wait_stream(side)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        outs = step()
+    for seed in (6, 7):
+        n = _inputs(seed, T, C, C, 1, F32, F32)
+        with torch.no_grad():
+            for t, v in zip(leaves, n[:3]):
+                t.copy_(v)
+        dh.copy_(n[3]), dl.copy_(n[4])
+        g.replay()
+        for p, q in zip(outs, _run(*n, None)):
+            assert torch.equal(p, q)
+
+
+def test_two_streams_at_once():
+    T, C = 20000, 64
+    sets = [_inputs(s, T, C, C, 1, F32, F32) for s in (1, 2)]
+    want = [_run(*s, None) for s in sets]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for _ in range(3):
+        got = []
+        for s, st in zip(sets, streams):
+            with torch.cuda.stream(st):
+                got.append(_run(*s, None))
+        torch.cuda.synchronize()
+        for g, w in zip(got, want):
+            for p, q in zip(g, w):
+                assert torch.equal(p, q)
+
+
+def test_bad_offsets_stay_inside_the_tensors():
+    """Offsets out of range or out of order: values are unspecified, but
+    nothing outside the outputs is written (host and kernel clamp them)."""
+    T, C = 3000, 8
+    a, x, h0, dh, dl = _inputs(5, T, C, C, 5, F32, F32)
+    for bad in ([0, 10, 5, 2000, 100, T], [-5, 0, 10, 20, 30, 10 ** 12], [T, T, T, T, T, T], [900, 800, 700, 2, 1, 0]):
+        off = torch.tensor(bad, dtype=torch.int64, device="cuda")
+        ws = GA.scan_workspace(a, x, off)
+        buf = torch.full((T + 128, C), 3.0, device="cuda")
+        last = torch.full((5 + 16, C), 3.0, device="cuda")
+        B.gs_scan_fwd(a, x, buf[64:T + 64], last[8:13], None, ws, h0, off)
+        assert (buf[:64] == 3).all() and (buf[T + 64:] == 3).all()
+        assert (last[:8] == 3).all() and (last[13:] == 3).all()
+        assert B.gs_read_status(ws) == B.GS_OK
+
+
+def test_no_rows():
+    h0 = torch.randn(3, 4, device="cuda")
+    off = torch.zeros(4, dtype=torch.int64, device="cuda")
+    a, x = torch.empty(0, 2, device="cuda"), torch.empty(0, 4, device="cuda")
+    leaves = [t.requires_grad_(True) for t in (a, x, h0)]
+    h, last = GA.gated_scan(*leaves, seq_offsets=off)
+    assert h.shape == (0, 4) and torch.equal(last, h0)
+    dl = torch.randn(3, 4, device="cuda")
+    assert torch.equal(torch.autograd.grad(last, leaves, dl)[2], dl)
+    h, last = GA.gated_scan(torch.empty(2, 0, 2, device="cuda"), torch.empty(2, 0, 4, device="cuda"))
+    assert (last == 0).all()
+
+
+@pytest.mark.slow
+def test_offsets_past_32_bits():
+    """A packed batch of more than 2^31 elements: its last sequence, and the
+    gradients of it, equal those of the sequence alone."""
+    C, tail = 512, 700
+    T = (1 << 31) // C + 40000
+    x = torch.zeros((T, C), dtype=BF16, device="cuda")
+    a = torch.full((T, 4), 0.5, device="cuda")
+    g = torch.Generator(device="cuda").manual_seed(0)
+    x[-tail:] = torch.randn((tail, C), generator=g, device="cuda").to(BF16)
+    a[-tail:] = torch.sigmoid(2 + torch.randn((tail, 4), generator=g, device="cuda"))
+    off = torch.tensor([0, T - tail, T], device="cuda")
+    dl = torch.randn((2, C), generator=g, device="cuda")
+    dh = torch.zeros_like(x)
+    h, last, da, dx, _ = _run(a, x, None, dh, dl, off)
+    an, xn = a[-tail:].clone(), x[-tail:].clone()
+    _check(an, xn, None, dh[-tail:], dl[1:], _offsets([tail]), False, False,
+           (h[-tail:], last[1:], da[-tail:], dx[-tail:], None))
+    assert (h[:T - tail:997] == 0).all()
+
+
+# -- single rows ------------------------------------------------------------
+
+@pytest.mark.parametrize("xdt,adt", [(F32, F32), (BF16, BF16), (BF16, F32), (F16, F16), (F16, F32)])
+@pytest.mark.parametrize("n,C,G", [(1, 1, 1), (1, 256, 256), (5, 37, 37), (33, 12, 3), (300, 1024, 16), (2, 7, 1)])
+@pytest.mark.parametrize("coupled", [False, True])
+def test_step(n, C, G, xdt, adt, coupled):
+    a, x, state, _, _ = _inputs(n + C, n, C, G, n, xdt, adt)
+    off = _offsets([1] * n)
+    want, last, _ = O.forward(_np(a), _np(x), off, _np(state), False, coupled)
+    mag = O.forward(_np(a), _np(x), off, _np(state), False, coupled, magnitude=True)[0]
+    h, new = GA.scan_step(a, x, state, coupled=coupled)
+    _within(h, want, mag, 4, xdt, "h")
+    _within(new, last, mag, 4, F32, "state")
+    kept = state.clone()
+    h2, out = GA.scan_step(a, x, kept, out_state=kept, coupled=coupled)
+    assert out.data_ptr() == kept.data_ptr() and torch.equal(kept, new) and torch.equal(h2, h)
+
+
+def test_steps_continue_a_scan():
+    """A prompt scanned at once and the rows after it one by one, by a
+    captured step, against the oracle over all rows."""
+    S, L, C = 4, 200, 64
+    a, x, _, _, _ = _inputs(8, S * L, C, C, S, F32, F32, h0=False)
+    args = (_np(a), _np(x), _offsets([L] * S))
+    want = O.forward(*args)[0].reshape(S, L, C)
+    mag = O.forward(*args, magnitude=True)[0].reshape(S, L, C)
+    a, x = a.view(S, L, C), x.view(S, L, C)
+    _, state = GA.gated_scan(a[:, :150].contiguous(), x[:, :150].contiguous())
+    ain, xin = a[:, 150].clone(), x[:, 150].clone()
+    warm = state.clone()
+    GA.scan_step(ain, xin, warm, out_state=warm)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        y, _ = GA.scan_step(ain, xin, state, out_state=state)
+    for t in range(150, L):
+        ain.copy_(a[:, t]), xin.copy_(x[:, t])
+        g.replay()
+        _within(y, want[:, t], mag[:, t], 2 * L + 64, F32, f"row {t}")
+
+
+def test_refusals():
+    a, x = torch.rand(8, 4, device="cuda"), torch.rand(8, 4, device="cuda")
+    off = torch.tensor([0, 8], device="cuda")
+    with pytest.raises(ValueError):
+        GA.gated_scan(a[:, :3].contiguous(), x)             # 3 gates do not divide 4 channels
+    with pytest.raises(ValueError):
+        GA.gated_scan(a[:4], x)
+    with pytest.raises(ValueError):
+        GA.gated_scan(a.double(), x.double())
+    with pytest.raises(ValueError):
+        GA.gated_scan(a.to(BF16), x)                        # 16-bit gates with fp32 inputs
+    with pytest.raises(ValueError):
+        GA.gated_scan(a.cpu(), x.cpu())
+    with pytest.raises(ValueError):
+        GA.gated_scan(a, x, seq_offsets=off.int())
+    with pytest.raises(ValueError):
+        GA.gated_scan(a, x, seq_offsets=off[:1])
+    with pytest.raises(ValueError):
+        GA.gated_scan(a.view(2, 4, 4), x.view(2, 4, 4), seq_offsets=off)
+    with pytest.raises(ValueError):
+        GA.gated_scan(a, x, h0=torch.zeros(2, 4, device="cuda"))
+    with pytest.raises(ValueError):
+        B.gs_scan_fwd(a, x.t(), torch.empty_like(x))        # rows not contiguous
+    with pytest.raises(ValueError):
+        B.gs_scan_fwd(a, x, torch.empty(8, 4, dtype=BF16, device="cuda"))
+    long = torch.rand(9000, 4, device="cuda")
+    with pytest.raises(B.GsError):
+        B.gs_scan_fwd(long, long, torch.empty_like(long))   # no workspace
+    with pytest.raises(B.GsError):
+        B.gs_scan_fwd(long, long, torch.empty_like(long), ws=torch.zeros(64, dtype=torch.uint8, device="cuda"))
+    with pytest.raises(ValueError):
+        GA.scan_step(a, x, torch.zeros(8, 4, dtype=BF16, device="cuda"))
+    with pytest.raises(ValueError):
+        GA.scan_step(a, x, torch.zeros(7, 4, device="cuda"))

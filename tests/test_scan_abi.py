@@ -1,0 +1,115 @@
+"""Host-side checks of the recurrence's and the gradient norm's entry points
+(no device: everything here is refused, or needs nothing, before a launch)."""
+import ctypes
+
+import pytest
+import torch
+
+from differentiable_gaussian_splatting_preprocess_b200 import binding as B
+from differentiable_gaussian_splatting_preprocess_b200 import build as BUILD
+
+P = ctypes.c_void_p
+
+
+@pytest.fixture(scope="module")
+def lib():
+    BUILD.build()
+    return B.lib()
+
+
+def _desc(rows=100, C=8, G=4, n_seq=1, **kw):
+    d = B.GsScanDesc(rows, C, G, n_seq, B.GS_F32, B.GS_F32, 0, G, C, C, G, C, C)
+    for k, v in kw.items():
+        setattr(d, k, v)
+    return d
+
+
+def test_struct_layouts():
+    # long long rows; int x6; long long x6
+    assert ctypes.sizeof(B.GsScanDesc) == 8 + 4 * 6 + 8 * 6
+    assert ctypes.sizeof(B.GsTensorList) == 8 + 3 * 8
+
+
+@pytest.mark.parametrize("kw", [dict(rows=-1), dict(channels=0), dict(gates=0), dict(gates=3), dict(n_seq=-1),
+                                dict(n_seq=0), dict(dtype=3), dict(gate_dtype=B.GS_F16), dict(flags=8),
+                                dict(stride_x=7), dict(stride_a=3), dict(stride_h=7), dict(stride_dx=0),
+                                dict(stride_da=-4), dict(stride_dh=1), dict(n_seq=7)])
+def test_bad_descriptions_are_refused(lib, kw):
+    d = _desc(**kw)
+    fake = P(4096)  # never dereferenced
+    big = 1 << 40
+    assert lib.gs_scan_fwd(ctypes.byref(d), fake, fake, None, None, fake, None, None, fake, big, None) \
+        == B.GS_ERR_INVALID_ARG
+    assert lib.gs_scan_bwd(ctypes.byref(d), fake, fake, None, None, fake, fake, None, fake, fake, None, fake, big,
+                           None) == B.GS_ERR_INVALID_ARG
+
+
+def test_missing_and_misaligned_pointers_are_refused(lib):
+    d, ok = _desc(rows=5000), P(4096)
+    need = lib.gs_scan_workspace_bytes(ctypes.byref(d))
+    assert need > 256
+    fwd = lambda a=ok, x=ok, h=ok, ws=ok, n=need, off=None: lib.gs_scan_fwd(  # noqa: E731
+        ctypes.byref(d), a, x, None, off, h, None, None, ws, n, None)
+    for kw in (dict(a=None), dict(x=None), dict(h=None), dict(ws=None), dict(n=need - 1), dict(ws=P(4104)),
+               dict(x=P(4098)), dict(off=P(4100))):
+        assert fwd(**kw) == B.GS_ERR_INVALID_ARG, kw
+    bwd = lambda states=ok, da=ok, dx=ok: lib.gs_scan_bwd(  # noqa: E731
+        ctypes.byref(d), ok, ok, None, None, states, ok, None, da, dx, None, ok, need, None)
+    for kw in (dict(states=None), dict(da=None), dict(dx=None), dict(dx=P(4097))):
+        assert bwd(**kw) == B.GS_ERR_INVALID_ARG, kw
+    one = _desc(rows=4, n_seq=4)
+    assert lib.gs_scan_step(ctypes.byref(one), ok, ok, None, ok, ok, None) == B.GS_ERR_INVALID_ARG
+    assert lib.gs_scan_step(ctypes.byref(_desc(rows=4, n_seq=2)), ok, ok, ok, ok, ok, None) == B.GS_ERR_INVALID_ARG
+    assert lib.gs_scan_fwd(None, ok, ok, None, None, ok, None, None, None, 0, None) == B.GS_ERR_INVALID_ARG
+
+
+def test_workspace_and_states_sizes(lib):
+    size = lambda **kw: lib.gs_scan_workspace_bytes(ctypes.byref(_desc(**kw)))  # noqa: E731
+    assert size(rows=1) == 0 and size(rows=0) == 0          # one tile: nothing to join
+    assert size(rows=10000) < size(rows=100000)
+    assert size(gates=3) == 0                               # invalid
+    assert lib.gs_scan_states_bytes(ctypes.byref(_desc(rows=1))) == 8 * 4
+    assert lib.gs_scan_states_bytes(ctypes.byref(_desc(rows=100000))) % (8 * 4) == 0
+
+
+def test_row_stride():
+    t = torch.zeros(6, 4, 8)
+    assert B.row_stride(t) == 8
+    assert B.row_stride(t[:, :, :5]) == 8
+    assert B.row_stride(t[:, :1, :5]) == 32
+    assert B.row_stride(torch.zeros(1, 8)[:, :3]) == 3
+    assert B.row_stride(torch.zeros(5, 1).expand(5, 1)) == 1
+    for bad in (t[:, :3], t.transpose(0, 1), torch.zeros(8, 4).t(), torch.zeros(1, 4).expand(5, 4), torch.zeros(3),
+                t[:, :, ::2]):
+        with pytest.raises(ValueError):
+            B.row_stride(bad)
+
+
+def _list(data, numel, dtype):
+    n = len(data)
+    return B.GsTensorList(n, (P * n)(*data), (ctypes.c_longlong * n)(*numel), (ctypes.c_int * n)(*dtype))
+
+
+def test_tensor_lists_are_checked(lib):
+    ok, ws, need = P(4096), P(8192), B.gs_grad_norm_workspace_bytes()
+    norm = lambda t, kind=0, out=ok, w=ws, n=need: lib.gs_grad_norm(  # noqa: E731
+        ctypes.byref(t) if t else None, kind, out, w, n, None)
+    good = _list([4096], [10], [B.GS_F32])
+    for args in (dict(t=None), dict(t=_list([None], [10], [0])), dict(t=_list([4096], [-1], [0])),
+                 dict(t=_list([4096], [10], [7])), dict(t=_list([4098], [10], [0])), dict(t=_list([4097], [10], [1])),
+                 dict(t=good, kind=2), dict(t=good, out=None), dict(t=good, w=None), dict(t=good, n=need - 1)):
+        assert norm(**args) == B.GS_ERR_INVALID_ARG, args
+    clip = lambda t, dst=None, out=ok, m=1.0, e=0.0: lib.gs_grad_clip(ctypes.byref(t), dst, out, m, e, None)  # noqa: E731
+    nan = float("nan")
+    for args in (dict(t=good, out=None), dict(t=good, m=-1.0), dict(t=good, m=nan), dict(t=good, e=-1.0),
+                 dict(t=good, dst=(P * 1)(None)), dict(t=good, dst=(P * 1)(4098))):
+        assert clip(**args) == B.GS_ERR_INVALID_ARG, args
+    assert clip(_list([None], [0], [0])) == B.GS_OK  # nothing to scale: nothing enqueued
+
+
+def test_clipped_adam_needs_a_norm(lib):
+    cfg = B.GsAdamConfig(1e-3, 1e-3, 1e-3, 1e-3, 1e-3, 0.9, 0.999, 1e-8, 0)
+    args = [ctypes.byref(cfg), 1, 0, 3] + [None] * 14
+    assert lib.gs_adam_step_clipped(*args, None, 1.0, 1e-6, None) == B.GS_ERR_INVALID_ARG
+    assert lib.gs_adam_step_clipped(*args, P(4096), -1.0, 1e-6, None) == B.GS_ERR_INVALID_ARG
+    assert lib.gs_adam_step_clipped(*args, P(4096), 1.0, 1e-6, None) == B.GS_OK  # N = 0: nothing to do
