@@ -16,6 +16,7 @@ import glob
 import os
 import subprocess
 import sys
+from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -54,7 +55,7 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False, 
     out_dir = os.path.join(OUT_DIR, "debug") if debug else OUT_DIR
     extra = ["-DGS_DEBUG", "-rdc=true"] if debug else []
     os.makedirs(out_dir, exist_ok=True)
-    objs = []
+    objs, cmds = [], []
     for src in sources():
         obj = os.path.join(out_dir, os.path.basename(src) + ".o")
         cmd = [NVCC, *ARCH, *CFLAGS, *extra, "-c", src, "-o", obj]
@@ -62,8 +63,10 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False, 
             cmd.insert(1, "-Xptxas=-v")
         if verbose:
             print(" ".join(cmd))
-        subprocess.run(cmd, check=True)
+        cmds.append(cmd)
         objs.append(obj)
+    with ThreadPoolExecutor(max_workers=os.cpu_count() or 1) as pool:  # one compiler per translation unit
+        list(pool.map(lambda c: subprocess.run(c, check=True), cmds))
     tmp = lib + f".tmp{os.getpid()}"
     cmd = [NVCC, *ARCH, *extra, "-shared", "-cudart", "static", "-o", tmp, *objs]
     if verbose:

@@ -1,0 +1,1565 @@
+// Kernels of the gated linear recurrence (scan.cu describes the operator).
+//
+// Two shapes of tile, both `runs` x rows per run by a block of channels:
+//  - wide (17 channels up): a warp is a run and its lanes are channels (V to a
+//    lane); a lane copies its own column to shared memory and back out.
+//  - narrow (up to 16 channels): a row is a few lanes or one, so a tile is
+//    staged through shared memory, where it arrives as one contiguous range,
+//    and a thread (or a few lanes) walks a run there.
+// Included by one translation unit per element type.
+#pragma once
+
+#include <climits>
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include "gs_internal.cuh"
+
+namespace gs {
+
+constexpr int kWideThreads = 128, kNarrowThreads = 256;
+// Rows per run.  At most 32: the start / finish bits of a run are one word.
+// Wide: long runs, since a warp's work per run beside its rows (finding the
+// tile, its marks, the joins) costs as much as a dozen rows.  Narrow: odd, so
+// that the runs of a warp start in different banks.
+#ifndef WRUN
+#define WRUN 32
+#endif
+#ifndef FMB
+#define FMB 3
+#endif
+#ifndef BMB
+#define BMB 4
+#endif
+#ifndef NGRP
+#define NGRP 4
+#endif
+constexpr int kWideRun = WRUN;
+constexpr int narrow_run(int v) { return v >= 3 ? 11 : 17; }
+constexpr unsigned kSpinLimit = 1u << 20;
+
+// How a tile's rows are moved: in 16-byte pieces of the whole tile (narrow
+// tiles whose rows are one contiguous range) or of each row (wide tiles), or
+// element by element.
+enum CopyMode { kFlat = 0, kRow16 = 1, kElem = 2 };
+
+struct ScanRecord {  // 16 bytes, published with one 128-bit store
+    float A, B;
+    unsigned tag;    // 2 * (epoch + 1) + (1 when B is the state itself)
+    unsigned pad;
+};
+constexpr int kGroup = 8;  // chunks of a group
+
+struct ScanParams {
+    long long rows, seq_len;
+    double seq_inv;            // 1 / seq_len
+    const long long* offsets;  // NULL: n_seq sequences of seq_len rows
+    long long sa, sx, sh, sda, sdx, sdh;
+    int C, G, group;           // group = C / G channels per gate
+    int n_seq, n_chunks, n_blocks;
+    int lpr_log2;              // narrow: lanes per row, as a power of two
+    int bc, bt;                // channels of a block, rows of a tile
+    int reverse, zero_pad, partial, part_gates;
+    int m_a, m_x, m_h, m_da, m_dx, m_dh;  // CopyMode
+    const void *a, *x, *dh;
+    const float *h0, *dh_last;
+    void *h, *da, *dx;
+    float *h_last, *states, *dh0, *part;
+    WsHeader* hdr;
+    ScanRecord *rec, *group_rec;  // per chunk, and per kGroup chunks
+};
+
+// Launches the scan (bwd: its adjoint) of one element type; `wide` and `v`
+// as chosen by the plan.
+int scan_launch_f32(const ScanParams& p, bool wide, int v, bool coupled, bool bwd, cudaStream_t s);
+int scan_launch_bf16(const ScanParams& p, bool gate_f32, bool wide, int v, bool coupled, bool bwd, cudaStream_t s);
+int scan_launch_f16(const ScanParams& p, bool gate_f32, bool wide, int v, bool coupled, bool bwd, cudaStream_t s);
+
+namespace {
+
+template <typename T> __device__ __forceinline__ float to_f(T v);
+template <> __device__ __forceinline__ float to_f<float>(float v) { return v; }
+template <> __device__ __forceinline__ float to_f<__half>(__half v) { return __half2float(v); }
+template <> __device__ __forceinline__ float to_f<__nv_bfloat16>(__nv_bfloat16 v) { return __bfloat162float(v); }
+template <typename T> __device__ __forceinline__ T from_f(float v);
+template <> __device__ __forceinline__ float from_f<float>(float v) { return v; }
+template <> __device__ __forceinline__ __half from_f<__half>(float v) { return __float2half_rn(v); }
+template <> __device__ __forceinline__ __nv_bfloat16 from_f<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
+
+// V neighbouring elements as loaded, and as fp32.
+template <typename T, int V> struct Pack;
+template <typename T> struct Pack<T, 1> {
+    T e;
+    __device__ __forceinline__ void load(const T* p) { e = *p; }
+    __device__ __forceinline__ void get(float (&f)[1]) const { f[0] = to_f<T>(e); }
+    __device__ static __forceinline__ void store(T* p, const float (&f)[1]) { *p = from_f<T>(f[0]); }
+};
+template <> struct Pack<float, 2> {
+    float2 e;
+    __device__ __forceinline__ void load(const float* p) { e = *reinterpret_cast<const float2*>(p); }
+    __device__ __forceinline__ void get(float (&f)[2]) const { f[0] = e.x, f[1] = e.y; }
+    __device__ static __forceinline__ void store(float* p, const float (&f)[2]) {
+        *reinterpret_cast<float2*>(p) = make_float2(f[0], f[1]);
+    }
+};
+template <> struct Pack<__nv_bfloat16, 2> {
+    unsigned e;
+    __device__ __forceinline__ void load(const __nv_bfloat16* p) { e = *reinterpret_cast<const unsigned*>(p); }
+    __device__ __forceinline__ void get(float (&f)[2]) const {
+        f[0] = __uint_as_float(e << 16), f[1] = __uint_as_float(e & 0xffff0000u);
+    }
+    __device__ static __forceinline__ void store(__nv_bfloat16* p, const float (&f)[2]) {
+        *reinterpret_cast<__nv_bfloat162*>(p) = __floats2bfloat162_rn(f[0], f[1]);
+    }
+};
+template <> struct Pack<__half, 2> {
+    unsigned e;
+    __device__ __forceinline__ void load(const __half* p) { e = *reinterpret_cast<const unsigned*>(p); }
+    __device__ __forceinline__ void get(float (&f)[2]) const {
+        __half2 t;
+        memcpy(&t, &e, 4);
+        const float2 q = __half22float2(t);
+        f[0] = q.x, f[1] = q.y;
+    }
+    __device__ static __forceinline__ void store(__half* p, const float (&f)[2]) {
+        *reinterpret_cast<__half2*>(p) = __floats2half2_rn(f[0], f[1]);
+    }
+};
+template <> struct Pack<__nv_bfloat16, 4> {
+    uint2 e;
+    __device__ __forceinline__ void load(const __nv_bfloat16* p) { e = *reinterpret_cast<const uint2*>(p); }
+    __device__ __forceinline__ void get(float (&f)[4]) const {
+        f[0] = __uint_as_float(e.x << 16), f[1] = __uint_as_float(e.x & 0xffff0000u);
+        f[2] = __uint_as_float(e.y << 16), f[3] = __uint_as_float(e.y & 0xffff0000u);
+    }
+    __device__ static __forceinline__ void store(__nv_bfloat16* p, const float (&f)[4]) {
+        const __nv_bfloat162 t[2] = {__floats2bfloat162_rn(f[0], f[1]), __floats2bfloat162_rn(f[2], f[3])};
+        uint2 w;
+        memcpy(&w, t, 8);
+        *reinterpret_cast<uint2*>(p) = w;
+    }
+};
+template <> struct Pack<__half, 4> {
+    uint2 e;
+    __device__ __forceinline__ void load(const __half* p) { e = *reinterpret_cast<const uint2*>(p); }
+    __device__ __forceinline__ void get(float (&f)[4]) const {
+        __half2 t[2];
+        memcpy(t, &e, 8);
+        const float2 q = __half22float2(t[0]), r = __half22float2(t[1]);
+        f[0] = q.x, f[1] = q.y, f[2] = r.x, f[3] = r.y;
+    }
+    __device__ static __forceinline__ void store(__half* p, const float (&f)[4]) {
+        const __half2 t[2] = {__floats2half2_rn(f[0], f[1]), __floats2half2_rn(f[2], f[3])};
+        uint2 w;
+        memcpy(&w, t, 8);
+        *reinterpret_cast<uint2*>(p) = w;
+    }
+};
+template <> struct Pack<float, 4> {
+    float4 e;
+    __device__ __forceinline__ void load(const float* p) { e = *reinterpret_cast<const float4*>(p); }
+    __device__ __forceinline__ void get(float (&f)[4]) const { f[0] = e.x, f[1] = e.y, f[2] = e.z, f[3] = e.w; }
+    __device__ static __forceinline__ void store(float* p, const float (&f)[4]) {
+        *reinterpret_cast<float4*>(p) = make_float4(f[0], f[1], f[2], f[3]);
+    }
+};
+template <> struct Pack<float, 3> {
+    float e[3];
+    __device__ __forceinline__ void load(const float* p) {
+#pragma unroll
+        for (int v = 0; v < 3; ++v) e[v] = p[v];
+    }
+    __device__ __forceinline__ void get(float (&f)[3]) const {
+#pragma unroll
+        for (int v = 0; v < 3; ++v) f[v] = e[v];
+    }
+    __device__ static __forceinline__ void store(float* p, const float (&f)[3]) {
+#pragma unroll
+        for (int v = 0; v < 3; ++v) p[v] = f[v];
+    }
+};
+
+// a b + c and a b per channel; pairs use the packed fp32 instructions (each
+// half rounds as the scalar one does).
+template <int V>
+__device__ __forceinline__ void fma_v(float (&d)[V], const float (&a)[V], const float (&b)[V], const float (&c)[V]) {
+    if constexpr (V % 2 == 0) {
+#pragma unroll
+        for (int v = 0; v < V; v += 2) {
+            const float2 r = __ffma2_rn(make_float2(a[v], a[v + 1]), make_float2(b[v], b[v + 1]), make_float2(c[v], c[v + 1]));
+            d[v] = r.x, d[v + 1] = r.y;
+        }
+    } else {
+#pragma unroll
+        for (int v = 0; v < V; ++v) d[v] = fmaf(a[v], b[v], c[v]);
+    }
+}
+template <int V> __device__ __forceinline__ void mul_v(float (&d)[V], const float (&a)[V], const float (&b)[V]) {
+    if constexpr (V % 2 == 0) {
+#pragma unroll
+        for (int v = 0; v < V; v += 2) {
+            const float2 r = __fmul2_rn(make_float2(a[v], a[v + 1]), make_float2(b[v], b[v + 1]));
+            d[v] = r.x, d[v + 1] = r.y;
+        }
+    } else {
+#pragma unroll
+        for (int v = 0; v < V; ++v) d[v] = a[v] * b[v];
+    }
+}
+template <int V> __device__ __forceinline__ void add_v(float (&d)[V], const float (&a)[V], const float (&b)[V]) {
+    if constexpr (V % 2 == 0) {
+#pragma unroll
+        for (int v = 0; v < V; v += 2) {
+            const float2 r = __fadd2_rn(make_float2(a[v], a[v + 1]), make_float2(b[v], b[v + 1]));
+            d[v] = r.x, d[v + 1] = r.y;
+        }
+    } else {
+#pragma unroll
+        for (int v = 0; v < V; ++v) d[v] = a[v] + b[v];
+    }
+}
+// (1 - a) x with one rounding: x - a x
+template <int V> __device__ __forceinline__ void rest_v(float (&d)[V], const float (&a)[V], const float (&x)[V]) {
+    float na[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) na[v] = -a[v];
+    fma_v<V>(d, na, x, x);
+}
+
+// A h + B, where a zero state contributes nothing even if the product of the
+// gates has overflowed (row by row, 0 * a is 0 for every finite gate; a gate
+// that is not finite is in B already).
+__device__ __forceinline__ float apply(float A, float B, float h) { return h == 0.0f ? B : fmaf(A, h, B); }
+
+__device__ __forceinline__ void publish(ScanRecord* p, float A, float B, unsigned tag) {
+    const unsigned long long lo = (unsigned long long)__float_as_uint(B) << 32 | __float_as_uint(A);
+    const unsigned long long hi = tag;
+    asm volatile("{ .reg .b128 q; mov.b128 q, {%1, %2}; st.relaxed.gpu.global.b128 [%0], q; }" ::"l"(p), "l"(lo),
+                 "l"(hi)
+                 : "memory");
+}
+
+__device__ __forceinline__ ScanRecord poll(const ScanRecord* p) {
+    unsigned long long lo, hi;
+    asm volatile("{ .reg .b128 q; ld.relaxed.gpu.global.b128 q, [%2]; mov.b128 {%0, %1}, q; }"
+                 : "=l"(lo), "=l"(hi)
+                 : "l"(p)
+                 : "memory");
+    ScanRecord r;
+    r.A = __uint_as_float((unsigned)lo);
+    r.B = __uint_as_float((unsigned)(lo >> 32));
+    r.tag = (unsigned)hi;
+    r.pad = 0;
+    return r;
+}
+
+__device__ __forceinline__ void cp_async16(void* smem, const void* gmem) {
+    const unsigned s = (unsigned)__cvta_generic_to_shared(smem);
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(s), "l"(gmem) : "memory");
+}
+__device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+
+// Row offset of sequence j (j = n_seq: the end), clamped to the tensor so
+// that bad offsets can give wrong values but no access out of range.
+__device__ __forceinline__ long long seq_row(const ScanParams& p, long long j) {
+    if (!p.offsets) return j * p.seq_len;
+    const long long v = p.offsets[j];
+    return v < 0 ? 0 : (v > p.rows ? p.rows : v);
+}
+
+// What the tile's rows are: per run the bits of rows that start (in scan
+// order) or finish a sequence, and per row the sequence.
+struct Marks {
+    unsigned* start;   // [runs]
+    unsigned* finish;  // [runs]
+    int* start_seq;    // [tile rows], valid where the bit is set
+    int* finish_seq;
+};
+
+// Which tile this block works on, and where it lies.
+struct Tile {
+    int k;            // chunk in the order the carry travels
+    int chunk;        // chunk in row order
+    int cb, c0, nc;   // channel block
+    int n;            // rows of this tile
+    int lo, hi;       // local range of the rows that belong to sequences
+    long long r0;
+    unsigned tag;     // record tag of an aggregate in this call
+};
+
+// First probe of the search for a tile's sequences, issued before the tile is
+// known: entry tid * step of the offsets, n_seq + 1 of them in NT steps.
+struct SeqProbe {
+    long long step, v;
+};
+template <int NT> __device__ __forceinline__ SeqProbe probe_seqs(const ScanParams& p) {
+    SeqProbe q;
+    const long long n = (long long)p.n_seq + 1;
+    q.step = (n + NT - 1) / NT;
+    const long long j = threadIdx.x * q.step;
+    q.v = p.offsets && j < n ? seq_row(p, j) : LLONG_MAX;
+    return q;
+}
+
+// Fills the marks of the tile's rows.  Sequences without rows pass their
+// first state on: `from` -> `to` for the tile's channels (every such sequence
+// belongs to exactly one chunk).  Called by the whole block.
+template <int RUN, int NT>
+__device__ __forceinline__ void mark_rows(const ScanParams& p, const Marks& mk, const Tile& t, SeqProbe q,
+                                          const float* from, float* to) {
+    const long long end = t.r0 + p.bt;
+    const bool last_chunk = t.chunk == p.n_chunks - 1;
+    // lo: no offset in front of entry lo reaches the tile, and the first that does is less than NT further
+    long long lo = 0;
+    if (p.offsets) {
+        long long n = (long long)p.n_seq + 1;
+        while (q.step > 1) {
+            // probes are increasing: the first `below` of them are in front of the tile
+            const int below = __syncthreads_count(q.v < t.r0);
+            if (below > 0) {
+                lo += (below - 1) * q.step + 1;
+                n = min(q.step - 1, (long long)p.n_seq + 1 - lo);
+            } else {
+                n = min(1ll, n);
+            }
+            q.step = (n + NT - 1) / NT;
+            const long long j = lo + threadIdx.x * q.step;
+            if (q.step > 1) q.v = j < lo + n ? seq_row(p, j) : LLONG_MAX;
+        }
+    } else if (p.seq_len > 0) {
+        // rows are below 2^40: the product is off by less than one sequence
+        lo = max((long long)((double)t.r0 * p.seq_inv) - 1, 0ll);
+    }
+    for (long long j = lo + threadIdx.x; j <= p.n_seq; j += NT) {
+        const long long v = seq_row(p, j);
+        const long long next = j < p.n_seq ? seq_row(p, j + 1) : v, prev = j > 0 ? seq_row(p, j - 1) : v;
+        if (v > end) break;
+        if (v < t.r0) continue;
+        if (j < p.n_seq && (v < end || last_chunk)) {
+            if (next > v) {
+                if (v < t.r0 + t.n) {
+                    const int pr = (int)(v - t.r0);
+                    const int l = p.reverse ? p.bt - 1 - pr : pr;
+                    (p.reverse ? mk.finish_seq : mk.start_seq)[pr] = (int)j;
+                    atomicOr(&(p.reverse ? mk.finish : mk.start)[l / RUN], 1u << (l % RUN));
+                }
+            } else if (to) {
+                for (int c = 0; c < t.nc; ++c) to[j * p.C + t.c0 + c] = from ? from[j * p.C + t.c0 + c] : 0.0f;
+            }
+        }
+        if (v > t.r0 && v <= t.r0 + t.n && prev < v) {
+            const int pr = (int)(v - 1 - t.r0);
+            const int l = p.reverse ? p.bt - 1 - pr : pr;
+            (p.reverse ? mk.start_seq : mk.finish_seq)[pr] = (int)(j - 1);
+            atomicOr(&(p.reverse ? mk.start : mk.finish)[l / RUN], 1u << (l % RUN));
+        }
+    }
+}
+
+// V neighbouring words of shared memory.
+template <int V> __device__ __forceinline__ void get_words(const float* p, float (&f)[V]) {
+    Pack<float, V> q;
+    q.load(p);
+    q.get(f);
+}
+
+// Shared words every tile kernel needs for the joins.
+struct Joins {
+    float *wA, *wB;   // [warps][bc] each warp's composite
+    float *carry;     // [bc] what comes in from the chunks before
+    int *flags;       // [0] a wait ran out, [1] ticket, [2] epoch
+    int *wf;          // [warps] whether the warp's composite absorbs
+};
+
+// Waits for a record of this call.  False when the wait ran out.
+__device__ __forceinline__ bool await(const ScanParams& p, const ScanRecord* q, unsigned tag, ScanRecord& r,
+                                      unsigned& spin) {
+    while ((r.tag | 1u) != (tag | 1u)) {
+        if (++spin > kSpinLimit || ((spin & 1023u) == 0 && *reinterpret_cast<volatile unsigned*>(&p.hdr->status))) {
+            raise_status(p.hdr, GS_ERR_TIMEOUT);
+            return false;
+        }
+        __nanosleep(20);
+        r = poll(q);
+    }
+    return true;
+}
+
+// Joins the tile to the chunks before it, given every warp's composite in
+// wA / wB / wf (first warp in travel order: 0 when `up`, else the last):
+// leaves the carry into the tile in m.carry (0 where the tile needs none: its
+// first row in travel order starts a sequence, or finishes one when the
+// carry travels down).  False when a wait ran out.
+//
+// One thread per channel.  A chunk publishes its composite at once.  Chunks
+// form groups of kGroup: the last one of a group publishes the group's
+// composite, and the state after the group when it knows it.  A chunk folds
+// the chunks of its own group before it, and looks back over whole groups to
+// the nearest whose state is known, kLookGroups of them in one round trip.
+// Every value is a fixed expression of the chunks' composites, whichever
+// groups happened to be finished, so equal inputs give equal bits.
+constexpr int kLookGroups = NGRP;
+
+template <int NT>
+__device__ __forceinline__ bool join_chunks(const ScanParams& p, const Tile& t, const Joins& m, bool up, bool needed) {
+    constexpr int kWarps = NT / 32;
+    const int tid = threadIdx.x, bc = p.bc;
+    if (p.n_chunks == 1) {
+        if (tid < bc) m.carry[tid] = 0.0f;
+        __syncthreads();
+        return true;
+    }
+    if (tid < bc) {
+        float A = 1.0f, B = 0.0f, carry = 0.0f;
+        bool known = t.k == 0;  // B is the state after this chunk, whatever comes in
+#pragma unroll
+        for (int i = 0; i < kWarps; ++i) {
+            const int w = up ? i : kWarps - 1 - i;
+            const float wa = m.wA[w * bc + tid], wb = m.wB[w * bc + tid];
+            if (m.wf[w]) B = wb, known = true;
+            else B = apply(wa, wb, B), A *= wa;
+        }
+        const size_t stride = (size_t)p.n_blocks * bc, at = (size_t)t.cb * bc + tid;
+        ScanRecord* rec = p.rec + (size_t)t.k * stride + at;
+        publish(rec, known ? 0.0f : A, B, t.tag | (known ? 1u : 0u));
+        const int g = t.k / kGroup, before = t.k % kGroup;
+        ScanRecord* grec = p.group_rec + (size_t)g * stride + at;
+        const bool closes = before == kGroup - 1;
+        if (known && closes) publish(grec, 0.0f, B, t.tag | 1u);
+        if (t.k > 0 && (needed || (closes && !known))) {
+            ScanRecord r[kGroup - 1], q[kLookGroups];
+#pragma unroll
+            for (int u = 0; u < kGroup - 1; ++u)
+                if (u < before) r[u] = poll(rec - (u + 1) * stride);
+#pragma unroll
+            for (int u = 0; u < kLookGroups; ++u)
+                if (u < g) q[u] = poll(grec - (u + 1) * stride);
+            // the chunks of this group before this one
+            unsigned spin = 0;
+            bool ok = true, stop = false;
+            int far = 0;  // how many of them count: up to the nearest whose state is known
+#pragma unroll
+            for (int u = 0; u < kGroup - 1; ++u) {
+                if (u >= before || stop || !ok) continue;
+                ok = await(p, rec - (u + 1) * stride, t.tag, r[u], spin);
+                stop = r[u].tag & 1u;
+                far = u + 1;
+            }
+            float PA = 1.0f, PB = 0.0f;
+#pragma unroll
+            for (int u = kGroup - 2; u >= 0; --u) {
+                if (u >= far) continue;
+                PB = apply(r[u].A, r[u].B, PB);
+                PA *= r[u].A;
+            }
+            const float GA = PA * A, GB = apply(A, B, PB);
+            if (ok && closes && !known) publish(grec, GA, GB, t.tag | (stop ? 1u : 0u));
+            carry = PB;
+            if (ok && !stop) {
+                // whole groups: wait until one of the window has its state, and those nearer their composites
+                int last = -1;
+                while (ok && last < 0) {
+                    bool gap = false;
+#pragma unroll
+                    for (int u = 0; u < kLookGroups; ++u) {
+                        if (u >= g || last >= 0 || gap) continue;
+                        if ((q[u].tag | 1u) != (t.tag | 1u)) gap = true;
+                        else if (q[u].tag & 1u) last = u;
+                    }
+                    if (last >= 0) break;
+                    if (++spin > kSpinLimit ||
+                        ((spin & 1023u) == 0 && *reinterpret_cast<volatile unsigned*>(&p.hdr->status))) {
+                        raise_status(p.hdr, GS_ERR_TIMEOUT);
+                        ok = false;
+                    }
+                    __nanosleep(20);
+#pragma unroll
+                    for (int u = 0; u < kLookGroups; ++u)
+                        if (u < g) q[u] = poll(grec - (u + 1) * stride);
+                }
+                float S = 0.0f;
+#pragma unroll
+                for (int u = kLookGroups - 1; u >= 0; --u) {
+                    if (u == last) S = q[u].B;
+                    else if (u < last) S = apply(q[u].A, q[u].B, S);
+                }
+                carry = apply(PA, PB, S);
+                if (ok && closes && !known) publish(grec, 0.0f, apply(GA, GB, S), t.tag | 1u);
+            }
+            if (!ok) m.flags[0] = 1;
+        }
+        m.carry[tid] = carry;
+    }
+    __syncthreads();
+    return m.flags[0] == 0;
+}
+
+// Takes a ticket.  Ticket and epoch share one 64-bit word of the workspace
+// (reserved[0..1]: ticket low, epoch high), read in one atomic; the block that
+// takes the call's last ticket leaves the word ready for the next call, whose
+// new epoch makes every record stale.
+__device__ __forceinline__ Tile begin_tile(const ScanParams& p, bool descending, int* flags) {
+    Tile t;
+    long long first = 0, end = p.rows;
+    if (p.offsets) first = seq_row(p, 0), end = seq_row(p, p.n_seq);
+    unsigned id = blockIdx.x, epoch = 0;
+    if (p.n_chunks > 1) {
+        if (threadIdx.x == 0) {
+            unsigned long long* word = reinterpret_cast<unsigned long long*>(p.hdr->reserved);
+            const unsigned long long w = atomicAdd(word, 1ull);
+            if ((unsigned)w == gridDim.x - 1) atomicAdd(word, (1ull << 32) - gridDim.x);
+            flags[1] = (int)(unsigned)w;
+            flags[2] = (int)(unsigned)(w >> 32);
+        }
+        __syncthreads();
+        id = (unsigned)flags[1];
+        epoch = (unsigned)flags[2];
+    }
+    t.tag = 2u * (epoch + 1u);
+    t.k = (int)(id / (unsigned)p.n_blocks);
+    t.cb = (int)(id - (unsigned)t.k * (unsigned)p.n_blocks);
+    t.chunk = descending ? p.n_chunks - 1 - t.k : t.k;
+    t.c0 = t.cb * p.bc;
+    t.nc = min(p.bc, p.C - t.c0);
+    t.r0 = (long long)t.chunk * p.bt;
+    t.n = (int)max(0ll, min((long long)p.bt, p.rows - t.r0));
+    t.lo = (int)min(max(first - t.r0, 0ll), (long long)t.n);
+    t.hi = (int)min(max(end - t.r0, (long long)t.lo), (long long)t.n);
+    return t;
+}
+
+// ---- wide tiles -----------------------------------------------------------
+
+constexpr int kWideWarps = kWideThreads / 32;
+constexpr int kWideRows = kWideWarps * kWideRun;
+constexpr unsigned kAllRows = kWideRun == 32 ? ~0u : (1u << kWideRun) - 1u;
+
+template <int V> struct WideShared {
+    float wA[kWideWarps * 32 * V], wB[kWideWarps * 32 * V], carry[32 * V];
+    unsigned start[kWideWarps], finish[kWideWarps];
+    int start_seq[kWideRows], finish_seq[kWideRows];
+    int flags[4], wf[kWideWarps];
+    __device__ Marks marks() { return {start, finish, start_seq, finish_seq}; }
+    __device__ Joins joins() { return {wA, wB, carry, flags, wf}; }
+};
+
+// Rows whose loads from shared memory are in flight together; left to itself
+// the compiler raises all rows' loads to the top and spills.
+constexpr int kStep = 4;
+__device__ __forceinline__ void step_fence(int r) {
+    if (r % kStep == 0) asm volatile("" ::: "memory");
+}
+
+// One tensor's rows of a warp's run in shared memory, copied there
+// asynchronously by the warp: in 16-byte pieces that bypass L1 where the rows
+// allow it (a tile's shared memory leaves L1 too small for the loads in
+// flight), else each lane its own elements.
+template <typename T, int V> struct Column {
+    T* run;  // first row of the run
+    T* s;    // this lane's element of it
+    static constexpr int kRow = 32 * V;
+    static constexpr int kBytes = kWideRows * kRow * (int)sizeof(T);
+    __device__ __forceinline__ Column(char* base, int warp, int lane)
+        : run(reinterpret_cast<T*>(base) + warp * kWideRun * kRow), s(run + lane * V) {}
+    __device__ __forceinline__ void copy(int r, const T* g) {
+        T* d = s + r * kRow;
+        if constexpr (V * sizeof(T) >= 4) {
+            const unsigned a = (unsigned)__cvta_generic_to_shared(d);
+            asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(a), "l"(g), "n"(V * (int)sizeof(T))
+                         : "memory");
+        } else {
+            *d = *g;
+        }
+    }
+    // Rows `live` of the run, `step` elements apart, of which this lane takes
+    // the elements at g; the others become `fill`.
+    __device__ __forceinline__ void load(const T* g, long long step, unsigned live, float fill) {
+        if (live == kAllRows) {
+#pragma unroll
+            for (int r = 0; r < kWideRun; ++r, g += step) copy(r, g);
+        } else {
+            for (int r = 0; r < kWideRun; ++r, g += step) {
+                if ((live >> r) & 1u) {
+                    copy(r, g);
+                } else {
+#pragma unroll
+                    for (int v = 0; v < V; ++v) s[r * kRow + v] = from_f<T>(fill);
+                }
+            }
+        }
+    }
+    // All rows of the run in 16-byte pieces; g: first of the block's `cols`
+    // columns.
+    __device__ __forceinline__ void load16(const T* g, long long step, int cols) {
+        constexpr int kPer = 16 / (int)sizeof(T), kLanes = kRow / kPer, kRows = 32 / kLanes;
+        const int lane = threadIdx.x & 31, piece = lane % kLanes, r0 = lane / kLanes;
+        if (piece * kPer >= cols) return;
+        T* d = run + r0 * kRow + piece * kPer;
+        g += r0 * step + piece * kPer;
+#pragma unroll
+        for (int r = 0; r < kWideRun; r += kRows, d += kRows * kRow, g += kRows * step)
+            if (kWideRun - r >= kRows || r + r0 < kWideRun) cp_async16(d, g);
+    }
+    __device__ __forceinline__ void get(int r, float (&f)[V]) const {
+        Pack<T, V> q;
+        q.load(s + r * kRow);
+        q.get(f);
+    }
+    __device__ __forceinline__ void put(int r, const float (&f)[V]) { Pack<T, V>::store(s + r * kRow, f); }
+};
+
+// Gates: V of them, or one for all V channels.
+template <typename AT, int V, bool SHARED> struct Gates : Column<AT, SHARED ? 1 : V> {
+    using Column<AT, SHARED ? 1 : V>::Column;
+    __device__ __forceinline__ void wide(int r, float (&f)[V]) const {
+        if constexpr (SHARED) {
+            float s[1];
+            this->get(r, s);
+#pragma unroll
+            for (int v = 0; v < V; ++v) f[v] = s[0];
+        } else {
+            this->get(r, f);
+        }
+    }
+};
+
+template <typename XT, typename AT, int V, bool SHARED>
+constexpr int wide_smem(bool bwd) {
+    return (int)(sizeof(WideShared<V>) + 15) / 16 * 16 + Gates<AT, V, SHARED>::kBytes +
+           Column<XT, V>::kBytes * (bwd ? 2 : 1);
+}
+
+// Bits r of the run's rows that exist and belong to a sequence.
+__device__ __forceinline__ unsigned live_rows(const ScanParams& p, const Tile& t, int l0) {
+    if (t.lo == 0 && t.hi == p.bt) return kAllRows;
+    unsigned m = 0;
+    for (int r = 0; r < kWideRun; ++r) {
+        const int pr = p.reverse ? p.bt - 1 - l0 - r : l0 + r;
+        if (pr >= t.lo && pr < t.hi) m |= 1u << r;
+    }
+    return m;
+}
+
+// Carry into warp `warp` of a wide tile from the tile's carry and the warps
+// before it (after it, when the carry travels down).
+template <int V>
+__device__ __forceinline__ void wide_carry(const WideShared<V>& sm, int warp, int ch, bool up, float (&h)[V]) {
+    for (int i = 0; i < kWideWarps; ++i) {
+        const int w = up ? i : kWideWarps - 1 - i;
+        if (w == warp) break;
+        float a[V], b[V];
+        get_words<V>(sm.wA + w * 32 * V + ch, a);
+        get_words<V>(sm.wB + w * 32 * V + ch, b);
+        const bool absorbs = sm.wf[w];
+#pragma unroll
+        for (int v = 0; v < V; ++v) h[v] = absorbs ? b[v] : apply(a[v], b[v], h[v]);
+    }
+}
+
+template <typename XT, typename AT, int V, bool SHARED, bool COUPLED>
+__global__ void __launch_bounds__(kWideThreads, FMB) k_scan_fwd_wide(const __grid_constant__ ScanParams p) {
+    extern __shared__ __align__(16) char smem[];
+    WideShared<V>& sm = *reinterpret_cast<WideShared<V>*>(smem);
+    char* data = smem + (sizeof(WideShared<V>) + 15) / 16 * 16;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const Joins m = sm.joins();
+    const SeqProbe probe = probe_seqs<kWideThreads>(p);
+    const Tile t = begin_tile(p, p.reverse, sm.flags);
+    if (tid < kWideWarps) sm.start[tid] = sm.finish[tid] = 0;
+    if (tid == 0) sm.flags[0] = 0;
+
+    const int ch = lane * V;
+    const bool active = ch < t.nc;
+    const int col = t.c0 + (active ? ch : 0);  // idle lanes repeat the first channel and store nothing
+    const int l0 = warp * kWideRun;
+    const unsigned live = live_rows(p, t, l0);
+    const long long row0 = t.r0 + (p.reverse ? p.bt - 1 - l0 : l0);
+    const int dir = p.reverse ? -1 : 1;
+    Gates<AT, V, SHARED> as(data, warp, lane);
+    Column<XT, V> xs(data + Gates<AT, V, SHARED>::kBytes, warp, lane);
+    const AT* ga = static_cast<const AT*>(p.a) + row0 * p.sa;
+    const XT* gx = static_cast<const XT*>(p.x) + row0 * p.sx;
+    if (!SHARED && p.m_a == kRow16 && live == kAllRows) as.load16(ga + t.c0, dir * p.sa, t.nc);
+    else as.load(ga + (p.group == 1 ? col : col / p.group), dir * p.sa, live, 1.0f);
+    if (p.m_x == kRow16 && live == kAllRows) xs.load16(gx + t.c0, dir * p.sx, t.nc);
+    else xs.load(gx + col, dir * p.sx, live, 0.0f);
+    __syncthreads();
+    mark_rows<kWideRun, kWideThreads>(p, sm.marks(), t, probe, p.h0, p.h_last);
+    cp_async_wait();
+    __syncthreads();
+    const unsigned starts = sm.start[warp], finishes = sm.finish[warp];
+    const bool plain = (starts | finishes) == 0 && live == kAllRows;
+
+    auto pr_of = [&](int r) { return p.reverse ? p.bt - 1 - l0 - r : l0 + r; };
+    auto first = [&](int r, float (&f)[V]) {
+#pragma unroll
+        for (int v = 0; v < V; ++v)
+            f[v] = p.h0 ? p.h0[(size_t)sm.start_seq[pr_of(r)] * p.C + col + v] : 0.0f;
+    };
+    auto row = [&](int r, float (&av)[V], float (&uv)[V]) {
+        as.wide(r, av);
+        xs.get(r, uv);
+        if (COUPLED) rest_v<V>(uv, av, uv);
+    };
+    float A[V], B[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) A[v] = 1.0f, B[v] = 0.0f;
+    if (plain) {
+#pragma unroll
+        for (int r = 0; r < kWideRun; ++r) {
+            step_fence(r);
+            float av[V], uv[V];
+            row(r, av, uv);
+            fma_v<V>(B, av, B, uv);
+            mul_v<V>(A, A, av);
+        }
+    } else {
+#pragma unroll kStep
+        for (int r = 0; r < kWideRun; ++r) {
+            float av[V], uv[V];
+            row(r, av, uv);
+            if ((starts >> r) & 1u) first(r, B);
+            fma_v<V>(B, av, B, uv);
+            mul_v<V>(A, A, av);
+        }
+    }
+    Pack<float, V>::store(sm.wA + warp * 32 * V + ch, A);
+    Pack<float, V>::store(sm.wB + warp * 32 * V + ch, B);
+    if (lane == 0) sm.wf[warp] = starts != 0;
+    __syncthreads();
+    if (!join_chunks<kWideThreads>(p, t, m, true, !(sm.start[0] & 1u))) return;
+    if (p.states && tid < t.nc) p.states[(size_t)t.chunk * p.C + t.c0 + tid] = sm.carry[tid];
+    float h[V];
+    get_words<V>(sm.carry + ch, h);
+    wide_carry<V>(sm, warp, ch, true, h);
+    XT* ph = static_cast<XT*>(p.h) + row0 * p.sh + col;
+    const long long dh = dir * p.sh;
+    if (!active) return;
+    if (plain) {
+        if (!p.h) return;
+#pragma unroll
+        for (int r = 0; r < kWideRun; ++r, ph += dh) {
+            step_fence(r);
+            float av[V], uv[V];
+            row(r, av, uv);
+            fma_v<V>(h, av, h, uv);
+            Pack<XT, V>::store(ph, h);
+        }
+        return;
+    }
+#pragma unroll kStep
+    for (int r = 0; r < kWideRun; ++r, ph += dh) {
+        float av[V], uv[V];
+        row(r, av, uv);
+        if ((starts >> r) & 1u) first(r, h);
+        fma_v<V>(h, av, h, uv);
+        if (p.h) {
+            if ((live >> r) & 1u) {
+                Pack<XT, V>::store(ph, h);
+            } else if (p.zero_pad && pr_of(r) < t.n) {
+                const float z[V] = {};
+                Pack<XT, V>::store(ph, z);
+            }
+        }
+        if (p.h_last && ((finishes >> r) & 1u)) {
+            float* q = p.h_last + (size_t)sm.finish_seq[pr_of(r)] * p.C + col;
+#pragma unroll
+            for (int v = 0; v < V; ++v) q[v] = h[v];
+        }
+    }
+}
+
+// Sums 8 rows' values over aligned groups of 2^bits lanes (one gate each): a
+// step adds half of the rows across one lane bit and leaves the other half to
+// the neighbour, so 8 rows cost 7 exchanges for 3 bits instead of 24.  Lane l
+// ends with the sums of rows (l mod 2^k) + 2^k i in s[i], k = min(bits, 3).
+__device__ __forceinline__ void sum_rows(float (&s)[8], int bits, int lane) {
+#pragma unroll
+    for (int b = 0; b < 3; ++b) {
+        if (b >= bits) break;
+        const bool hi = (lane >> b) & 1;
+#pragma unroll
+        for (int i = 0; i < (4 >> b); ++i) {
+            const float keep = hi ? s[2 * i + 1] : s[2 * i], give = hi ? s[2 * i] : s[2 * i + 1];
+            s[i] = keep + __shfl_xor_sync(~0u, give, 1 << b);
+        }
+    }
+    if (bits > 3) s[0] += __shfl_xor_sync(~0u, s[0], 8);
+    if (bits > 4) s[0] += __shfl_xor_sync(~0u, s[0], 16);
+}
+
+template <typename XT, typename AT, int V, bool SHARED, bool COUPLED>
+__global__ void __launch_bounds__(kWideThreads, BMB) k_scan_bwd_wide(const __grid_constant__ ScanParams p) {
+    extern __shared__ __align__(16) char smem[];
+    WideShared<V>& sm = *reinterpret_cast<WideShared<V>*>(smem);
+    char* data = smem + (sizeof(WideShared<V>) + 15) / 16 * 16;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const Joins m = sm.joins();
+    const SeqProbe probe = probe_seqs<kWideThreads>(p);
+    const Tile t = begin_tile(p, !p.reverse, sm.flags);
+    if (tid < kWideWarps) sm.start[tid] = sm.finish[tid] = 0;
+    if (tid == 0) sm.flags[0] = 0;
+
+    const int ch = lane * V;
+    const bool active = ch < t.nc;
+    const int col = t.c0 + (active ? ch : 0);
+    const int gcol = p.group == 1 ? col : col / p.group;
+    const int l0 = warp * kWideRun;
+    const unsigned live = live_rows(p, t, l0);
+    const long long row0 = t.r0 + (p.reverse ? p.bt - 1 - l0 : l0);
+    const int dir = p.reverse ? -1 : 1;
+    Gates<AT, V, SHARED> as(data, warp, lane);
+    Column<XT, V> xs(data + Gates<AT, V, SHARED>::kBytes, warp, lane);
+    Column<XT, V> ds(data + Gates<AT, V, SHARED>::kBytes + Column<XT, V>::kBytes, warp, lane);
+    const AT* ga = static_cast<const AT*>(p.a) + row0 * p.sa;
+    const XT* gx = static_cast<const XT*>(p.x) + row0 * p.sx;
+    if (!SHARED && p.m_a == kRow16 && live == kAllRows) as.load16(ga + t.c0, dir * p.sa, t.nc);
+    else as.load(ga + gcol, dir * p.sa, live, 1.0f);
+    if (p.m_x == kRow16 && live == kAllRows) xs.load16(gx + t.c0, dir * p.sx, t.nc);
+    else xs.load(gx + col, dir * p.sx, live, 0.0f);
+    const XT* gd = static_cast<const XT*>(p.dh) + row0 * p.sdh;
+    if (p.m_dh == kRow16 && p.dh && live == kAllRows) ds.load16(gd + t.c0, dir * p.sdh, t.nc);
+    else ds.load(gd + col, dir * p.sdh, p.dh ? live : 0u, 0.0f);
+    __syncthreads();
+    mark_rows<kWideRun, kWideThreads>(p, sm.marks(), t, probe, p.dh_last, p.dh0);
+    cp_async_wait();
+    __syncthreads();
+    const unsigned starts = sm.start[warp], finishes = p.dh_last ? sm.finish[warp] : 0u;
+    const bool plain = (starts | finishes) == 0 && live == kAllRows;
+
+    auto pr_of = [&](int r) { return p.reverse ? p.bt - 1 - l0 - r : l0 + r; };
+    auto first = [&](int r, float (&f)[V]) {
+#pragma unroll
+        for (int v = 0; v < V; ++v)
+            f[v] = p.h0 ? p.h0[(size_t)sm.start_seq[pr_of(r)] * p.C + col + v] : 0.0f;
+    };
+    // gradient a row's state receives from outside the recurrence
+    auto upstream = [&](int r, float (&f)[V]) {
+        ds.get(r, f);
+        if ((finishes >> r) & 1u) {
+#pragma unroll
+            for (int v = 0; v < V; ++v) f[v] += p.dh_last[(size_t)sm.finish_seq[pr_of(r)] * p.C + col + v];
+        }
+    };
+    // The run's action on the state (A, B) and on the adjoint (A, K), and the
+    // former at the run's parts of kPart rows: the states in front of a part's
+    // rows are formed again when the adjoint gets there, a part at a time.
+    constexpr int kPart = 8, kParts = (kWideRun + kPart - 1) / kPart;
+    float A[V], B[V], K[V], Ap[kParts][V], Bp[kParts][V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) A[v] = 1.0f, B[v] = 0.0f, K[v] = 0.0f;
+    if (plain) {
+        // the adjoint leaves the run as the sum of dh times the gates up to it: one pass gives all three
+#pragma unroll
+        for (int r = 0; r < kWideRun; ++r) {
+            step_fence(r);
+            if (r % kPart == 0) {
+#pragma unroll
+                for (int v = 0; v < V; ++v) Ap[r / kPart][v] = A[v], Bp[r / kPart][v] = B[v];
+            }
+            float av[V], uv[V], dv[V];
+            as.wide(r, av);
+            xs.get(r, uv);
+            ds.get(r, dv);
+            if (COUPLED) rest_v<V>(uv, av, uv);
+            fma_v<V>(B, av, B, uv);
+            mul_v<V>(A, A, av);
+            fma_v<V>(K, A, dv, K);
+        }
+    } else {
+#pragma unroll
+        for (int part = 0; part < kParts; ++part) {
+#pragma unroll
+            for (int v = 0; v < V; ++v) Ap[part][v] = A[v], Bp[part][v] = B[v];
+#pragma unroll kStep
+            for (int r = part * kPart; r < min(kWideRun, (part + 1) * kPart); ++r) {
+                float av[V], uv[V];
+                as.wide(r, av);
+                xs.get(r, uv);
+                if (COUPLED) rest_v<V>(uv, av, uv);
+                if ((starts >> r) & 1u) first(r, B);
+                fma_v<V>(B, av, B, uv);
+                mul_v<V>(A, A, av);
+            }
+        }
+#pragma unroll kStep
+        for (int r = kWideRun - 1; r >= 0; --r) {
+            float av[V], dv[V];
+            as.wide(r, av);
+            upstream(r, dv);
+            add_v<V>(K, K, dv);
+            mul_v<V>(K, K, av);
+            if ((starts >> r) & 1u) {
+#pragma unroll
+                for (int v = 0; v < V; ++v) K[v] = 0.0f;
+            }
+        }
+    }
+    // the state in front of this warp's run
+    Pack<float, V>::store(sm.wA + warp * 32 * V + ch, A);
+    Pack<float, V>::store(sm.wB + warp * 32 * V + ch, B);
+    if (lane == 0) sm.wf[warp] = starts != 0;
+    float h[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) h[v] = p.states[(size_t)t.chunk * p.C + col + v];
+    __syncthreads();
+    wide_carry<V>(sm, warp, ch, true, h);
+    __syncthreads();
+    Pack<float, V>::store(sm.wB + warp * 32 * V + ch, K);
+    __syncthreads();
+    if (!join_chunks<kWideThreads>(p, t, m, false, !(sm.finish[kWideWarps - 1] >> (kWideRun - 1) & 1u))) return;
+    get_words<V>(sm.carry + ch, K);
+    wide_carry<V>(sm, warp, ch, false, K);
+    const long long sdx = dir * p.sdx, sda = dir * p.sda, spart = dir * p.part_gates;
+    const long long end = row0 + dir * kWideRun;  // one row past the run
+    XT* pdx = static_cast<XT*>(p.dx) + end * p.sdx + col;
+    AT* pda = static_cast<AT*>(p.da) + end * p.sda + gcol;
+    const unsigned store = active ? live : 0u;
+    // What a gate's gradient multiplies: the state before the row (coupled:
+    // less x), for the rows of one part.
+    float hp[kPart][V];
+    auto states_of = [&](int part) {
+        float hs[V];
+        const bool cut = starts & ((1u << (part * kPart)) - 1u);
+#pragma unroll
+        for (int v = 0; v < V; ++v) hs[v] = cut ? Bp[part][v] : apply(Ap[part][v], Bp[part][v], h[v]);
+#pragma unroll
+        for (int i = 0; i < kPart; ++i) {
+            const int r = part * kPart + i;
+            if (r >= kWideRun) continue;
+            step_fence(r);
+            float av[V], uv[V];
+            as.wide(r, av);
+            xs.get(r, uv);
+            if (!plain && ((starts >> r) & 1u)) first(r, hs);
+#pragma unroll
+            for (int v = 0; v < V; ++v) hp[i][v] = COUPLED ? hs[v] - uv[v] : hs[v];
+            if (COUPLED) rest_v<V>(uv, av, uv);
+            fma_v<V>(hs, av, hs, uv);
+        }
+    };
+    // the adjoint of row r: writes dx, returns the products of the gate's gradient
+    auto reverse_row = [&](int r, float (&dav)[V]) {
+        float av[V], g[V], dxv[V];
+        as.wide(r, av);
+        if (plain) ds.get(r, g);
+        else upstream(r, g);
+        add_v<V>(g, g, K);
+        mul_v<V>(dav, g, hp[r % kPart]);
+        if (COUPLED) {
+            rest_v<V>(dxv, av, g);
+        } else {
+#pragma unroll
+            for (int v = 0; v < V; ++v) dxv[v] = g[v];
+        }
+        mul_v<V>(K, av, g);
+        if (!plain && ((starts >> r) & 1u)) {
+            if (p.dh0 && active) {
+                float* d = p.dh0 + (size_t)sm.start_seq[pr_of(r)] * p.C + col;
+#pragma unroll
+                for (int v = 0; v < V; ++v) d[v] = K[v];
+            }
+#pragma unroll
+            for (int v = 0; v < V; ++v) K[v] = 0.0f;
+        }
+        pdx -= sdx;
+        if ((store >> r) & 1u) Pack<XT, V>::store(pdx, dxv);
+    };
+    const bool shared = SHARED || p.group > 1;
+    float* part_sum = p.part;
+    if (p.partial) part_sum += ((long long)t.cb * p.rows + row0) * p.part_gates + gcol - t.c0 / p.group;
+    if (!shared) {
+        if constexpr (!SHARED) {
+#pragma unroll
+            for (int part = kParts - 1; part >= 0; --part) {
+                states_of(part);
+#pragma unroll
+                for (int i = kPart - 1; i >= 0; --i) {
+                    const int r = part * kPart + i;
+                    if (r >= kWideRun) continue;
+                    step_fence(r);
+                    float dav[V];
+                    reverse_row(r, dav);
+                    pda -= sda;
+                    if ((store >> r) & 1u) Pack<AT, V>::store(pda, dav);
+                }
+            }
+        }
+    } else {
+        pda -= kWideRun * sda;
+        auto write = [&](int r, float v) {
+            if (!((live >> r) & 1u)) return;
+            if (p.partial) part_sum[r * spart] = v;
+            else pda[r * sda] = from_f<AT>(v);
+        };
+        // lanes of one gate: the whole warp, an aligned group of a power of two, or any run of lanes
+        const int gl = p.group / V;
+        const bool whole = t.c0 / p.group == (t.c0 + t.nc - 1) / p.group;
+        const bool even = whole || (gl < 32 && (gl & (gl - 1)) == 0 && gl * V == p.group);
+        const int bits = whole ? 5 : 31 - __clz(gl), nb = min(bits, 3);
+        const bool writes = (whole || active) && (lane & ((1 << bits) - 1)) < kPart;  // idle lanes hold sums too
+        unsigned same = 0;
+        if (active && !even) {
+#pragma unroll
+            for (int i = 0; i < 5; ++i) {
+                const int o = lane + (1 << i);
+                if (o < 32 && o * V < t.nc && (t.c0 + o * V) / p.group == gcol) same |= 1u << i;
+            }
+        }
+        const bool head = active && (lane == 0 || (col - V) / p.group != gcol);
+#pragma unroll
+        for (int part = kParts - 1; part >= 0; --part) {
+            states_of(part);
+            float s[kPart];
+#pragma unroll
+            for (int i = kPart - 1; i >= 0; --i) {
+                const int r = part * kPart + i;
+                s[i] = 0.0f;
+                if (r >= kWideRun) continue;
+                step_fence(r);
+                float dav[V];
+                reverse_row(r, dav);
+                if (active) {
+#pragma unroll
+                    for (int v = 0; v < V; ++v) s[i] += dav[v];
+                }
+            }
+            if (even) {
+                sum_rows(s, bits, lane);
+#pragma unroll
+                for (int i = 0; i < kPart; ++i)
+                    if ((i << nb) < kPart && writes) write(part * kPart + (lane & ((1 << nb) - 1)) + (i << nb), s[i]);
+            } else {
+#pragma unroll
+                for (int i = 0; i < kPart; ++i) {
+                    float v = s[i];
+#pragma unroll
+                    for (int b = 0; b < 5; ++b) {
+                        const float o = __shfl_down_sync(~0u, v, 1 << b);
+                        if ((same >> b) & 1u) v += o;
+                    }
+                    if (head) write(part * kPart + i, v);
+                }
+            }
+        }
+    }
+    if (p.zero_pad && active && live != kAllRows) {
+        const float z[V] = {};
+        for (int r = 0; r < kWideRun; ++r, pdx += sdx, pda += sda) {
+            if (((live >> r) & 1u) || pr_of(r) >= t.n) continue;
+            Pack<XT, V>::store(pdx, z);
+            if (p.partial) continue;
+            if constexpr (SHARED || V == 1) {
+                *pda = from_f<AT>(0.0f);  // lanes of one gate write the same zero
+            } else {
+                Pack<AT, V>::store(pda, z);
+            }
+        }
+    }
+}
+
+// ---- narrow tiles ---------------------------------------------------------
+
+constexpr int kNarrowWarps = kNarrowThreads / 32;
+
+// Carry into warp `warp` from the tile's carry and the warps before it (after
+// it, when the carry travels down).
+__device__ __forceinline__ float warp_carry(const ScanParams& p, const Joins& m, int warp, int ch, float h, bool up) {
+    if (up)
+        for (int w = 0; w < warp; ++w)
+            h = m.wf[w] ? m.wB[w * p.bc + ch] : apply(m.wA[w * p.bc + ch], m.wB[w * p.bc + ch], h);
+    else
+        for (int w = kNarrowWarps - 1; w > warp; --w)
+            h = m.wf[w] ? m.wB[w * p.bc + ch] : apply(m.wA[w * p.bc + ch], m.wB[w * p.bc + ch], h);
+    return h;
+}
+
+// Tile -> shared memory: rows of `cols` elements, one block of channels.
+// Rows outside [lo, hi) (local) belong to no sequence, rows from n on do not
+// exist: they become `fill`.
+template <typename T>
+__device__ void load_tile(T* tile, const T* g, long long stride, const Tile& t, int bt, int cols, int mode,
+                          float fill) {
+    const int tid = threadIdx.x;
+    constexpr int kPer = 16 / sizeof(T);
+    const int total = t.n * cols;
+    if (mode == kFlat && t.lo == 0 && t.hi == t.n) {
+        const int vecs = total / kPer;
+        const T* src = g + t.r0 * stride;
+        for (int i = tid; i < vecs; i += kNarrowThreads) cp_async16(tile + i * kPer, src + i * kPer);
+        for (int i = vecs * kPer + tid; i < total; i += kNarrowThreads) tile[i] = src[i];
+    } else {
+        for (int i = tid; i < total; i += kNarrowThreads) {
+            const int r = i / cols, c = i - r * cols;
+            tile[i] = (r >= t.lo && r < t.hi) ? g[(t.r0 + r) * stride + c] : from_f<T>(fill);
+        }
+    }
+    for (int i = total + tid; i < bt * cols; i += kNarrowThreads) tile[i] = from_f<T>(fill);
+}
+
+// Shared memory -> tile; rows of no sequence are left as they were, or
+// zeroed.
+template <typename T>
+__device__ void store_tile(const T* tile, T* g, long long stride, const Tile& t, int cols, int mode, int zero_pad) {
+    const int tid = threadIdx.x;
+    constexpr int kPer = 16 / sizeof(T);
+    const int total = t.n * cols;
+    if (mode == kFlat && t.lo == 0 && t.hi == t.n) {
+        const int vecs = total / kPer;
+        T* dst = g + t.r0 * stride;
+        for (int i = tid; i < vecs; i += kNarrowThreads)
+            reinterpret_cast<uint4*>(dst)[i] = reinterpret_cast<const uint4*>(tile)[i];
+        for (int i = vecs * kPer + tid; i < total; i += kNarrowThreads) dst[i] = tile[i];
+    } else {
+        for (int i = tid; i < total; i += kNarrowThreads) {
+            const int r = i / cols, c = i - r * cols;
+            const bool in = r >= t.lo && r < t.hi;
+            if (in || zero_pad) g[(t.r0 + r) * stride + c] = in ? tile[i] : from_f<T>(0.0f);
+        }
+    }
+}
+
+struct NarrowMem {
+    char *x, *a, *g;
+    Marks mk;
+    Joins j;
+};
+
+// Bytes of (and, on the device, pointers into) the dynamic shared memory.
+__host__ __device__ inline size_t narrow_mem(const ScanParams& p, int xs, int as, bool bwd, char* base,
+                                             NarrowMem* m) {
+    const int runs = kNarrowThreads >> p.lpr_log2;
+    size_t o = 0;
+    auto take = [&](size_t bytes) {
+        char* r = base + o;
+        o += (bytes + 15) / 16 * 16;
+        return r;
+    };
+    char* x = take((size_t)p.bt * p.C * xs);
+    char* a = take((size_t)p.bt * p.G * as);
+    char* g = bwd && p.dh ? take((size_t)p.bt * p.C * xs) : base;
+    char* s0 = take((size_t)runs * 4);
+    char* s1 = take((size_t)runs * 4);
+    char* s2 = take((size_t)p.bt * 4);
+    char* s3 = take((size_t)p.bt * 4);
+    char* wa = take((size_t)kNarrowWarps * p.bc * 4);
+    char* wb = take((size_t)kNarrowWarps * p.bc * 4);
+    char* ca = take((size_t)p.bc * 4);
+    char* fl = take(16);
+    char* wf = take(kNarrowWarps * 4);
+    if (m) {
+        m->x = x;
+        m->a = a;
+        m->g = g;
+        m->mk = {reinterpret_cast<unsigned*>(s0), reinterpret_cast<unsigned*>(s1), reinterpret_cast<int*>(s2),
+                 reinterpret_cast<int*>(s3)};
+        m->j = {reinterpret_cast<float*>(wa), reinterpret_cast<float*>(wb), reinterpret_cast<float*>(ca),
+                reinterpret_cast<int*>(fl), reinterpret_cast<int*>(wf)};
+    }
+    return o;
+}
+
+// Composites of the runs of one warp, and of what lies before (up) or behind
+// (down) this lane's run inside the warp; the warp's own goes to wA/wB/wf.
+template <int V>
+__device__ __forceinline__ void join_runs(const ScanParams& p, const Joins& m, bool up, int ch, int f, float (&A)[V],
+                                          float (&B)[V], int& fe, float (&Ae)[V], float (&Be)[V]) {
+    const int lane32 = threadIdx.x & 31, warp = threadIdx.x >> 5, lpr = 1 << p.lpr_log2;
+    auto shift = [&](auto v, int d) { return up ? __shfl_up_sync(~0u, v, d) : __shfl_down_sync(~0u, v, d); };
+    auto has = [&](int d) { return up ? lane32 >= d : lane32 + d < 32; };
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        if (d < lpr) continue;
+        const int fo = shift(f, d);
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            const float Ao = shift(A[v], d), Bo = shift(B[v], d);
+            if (has(d) && !f) {
+                B[v] = apply(A[v], B[v], Bo);
+                A[v] *= Ao;
+            }
+        }
+        if (has(d)) f |= fo;
+    }
+    if (up ? lane32 >= 32 - lpr : lane32 < lpr) {
+#pragma unroll
+        for (int v = 0; v < V; ++v) m.wA[warp * p.bc + ch + v] = A[v], m.wB[warp * p.bc + ch + v] = B[v];
+        m.wf[warp] = f;
+    }
+    fe = shift(f, lpr);
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+        Ae[v] = shift(A[v], lpr);
+        Be[v] = shift(B[v], lpr);
+        if (!has(lpr)) Ae[v] = 1.0f, Be[v] = 0.0f;
+    }
+    if (!has(lpr)) fe = 0;
+}
+
+template <typename XT, typename AT, int V, bool COUPLED>
+__global__ void __launch_bounds__(kNarrowThreads, V == 1 ? 4 : 3) k_scan_fwd_narrow(const __grid_constant__ ScanParams p) {
+    constexpr int RUN = narrow_run(V);
+    extern __shared__ __align__(16) char smem[];
+    NarrowMem m;
+    narrow_mem(p, sizeof(XT), sizeof(AT), false, smem, &m);
+    const int tid = threadIdx.x, warp = tid >> 5;
+    const int runs = kNarrowThreads >> p.lpr_log2;
+    const int run = tid >> p.lpr_log2, lane = tid & ((1 << p.lpr_log2) - 1);
+    const SeqProbe probe = probe_seqs<kNarrowThreads>(p);
+    const Tile t = begin_tile(p, p.reverse, m.j.flags);
+    XT* sx = reinterpret_cast<XT*>(m.x);
+    AT* sa = reinterpret_cast<AT*>(m.a);
+    load_tile(sx, static_cast<const XT*>(p.x), p.sx, t, p.bt, p.C, p.m_x, 0.0f);
+    load_tile(sa, static_cast<const AT*>(p.a), p.sa, t, p.bt, p.G, p.m_a, 1.0f);
+    for (int i = tid; i < runs; i += kNarrowThreads) m.mk.start[i] = m.mk.finish[i] = 0;
+    if (tid == 0) m.j.flags[0] = 0;
+    __syncthreads();
+    mark_rows<RUN, kNarrowThreads>(p, m.mk, t, probe, p.h0, p.h_last);
+    cp_async_wait();
+    __syncthreads();
+
+    const int ch = lane * V;
+    const bool active = ch < t.nc;
+    const int col = active ? ch : 0;
+    const unsigned starts = m.mk.start[run], finishes = p.h_last && active ? m.mk.finish[run] : 0u;
+    const int l0 = run * RUN, step = p.reverse ? -1 : 1;
+    const int pr0 = p.reverse ? p.bt - 1 - l0 : l0;
+    XT* px = sx + pr0 * p.C + col;
+    const AT* pa = sa + pr0 * p.G + col / p.group;
+    const int dx = step * p.C, da = step * p.G;
+    auto row = [&](int r, float (&av)[V], float (&uv)[V]) {
+        Pack<XT, V> xv;
+        xv.load(px + r * dx);
+        xv.get(uv);
+        const float a0 = to_f<AT>(pa[r * da]);  // V > 1: the channels of a lane share their gate
+#pragma unroll
+        for (int v = 0; v < V; ++v) av[v] = a0;
+        if (COUPLED) rest_v<V>(uv, av, uv);
+    };
+    auto first = [&](int r, float (&f)[V]) {
+#pragma unroll
+        for (int v = 0; v < V; ++v)
+            f[v] = p.h0 ? p.h0[(size_t)m.mk.start_seq[pr0 + step * r] * p.C + col + v] : 0.0f;
+    };
+    float A[V], B[V], Ae[V], Be[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) A[v] = 1.0f, B[v] = 0.0f;
+#pragma unroll 6
+    for (int r = 0; r < RUN; ++r) {
+        float av[V], uv[V];
+        row(r, av, uv);
+        if ((starts >> r) & 1u) first(r, B);
+        fma_v<V>(B, av, B, uv);
+        mul_v<V>(A, A, av);
+    }
+    int fe;
+    join_runs<V>(p, m.j, true, ch, starts != 0, A, B, fe, Ae, Be);
+    __syncthreads();
+    if (join_chunks<kNarrowThreads>(p, t, m.j, true, !(m.mk.start[0] & 1u))) {
+        if (p.states && tid < t.nc) p.states[(size_t)t.chunk * p.C + tid] = m.j.carry[tid];
+        float h[V];
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            h[v] = warp_carry(p, m.j, warp, ch + v, m.j.carry[ch + v], true);
+            h[v] = fe ? Be[v] : apply(Ae[v], Be[v], h[v]);
+        }
+        const bool keep = p.h && active;
+#pragma unroll 6
+        for (int r = 0; r < RUN; ++r) {
+            float av[V], uv[V];
+            row(r, av, uv);
+            if ((starts >> r) & 1u) first(r, h);
+            fma_v<V>(h, av, h, uv);
+            if (keep) Pack<XT, V>::store(px + r * dx, h);
+            if ((finishes >> r) & 1u) {
+                float* q = p.h_last + (size_t)m.mk.finish_seq[pr0 + step * r] * p.C + col;
+#pragma unroll
+                for (int v = 0; v < V; ++v) q[v] = h[v];
+            }
+        }
+        if (p.h) {
+            __syncthreads();
+            store_tile(sx, static_cast<XT*>(p.h), p.sh, t, p.C, p.m_h, p.zero_pad);
+        }
+    }
+}
+
+template <typename XT, typename AT, int V, bool COUPLED>
+__global__ void __launch_bounds__(kNarrowThreads, V == 1 ? 4 : 3) k_scan_bwd_narrow(const __grid_constant__ ScanParams p) {
+    constexpr int RUN = narrow_run(V);
+    extern __shared__ __align__(16) char smem[];
+    NarrowMem m;
+    narrow_mem(p, sizeof(XT), sizeof(AT), true, smem, &m);
+    const int tid = threadIdx.x, warp = tid >> 5;
+    const int lpr = 1 << p.lpr_log2, runs = kNarrowThreads >> p.lpr_log2;
+    const int run = tid >> p.lpr_log2, lane = tid & (lpr - 1);
+    const SeqProbe probe = probe_seqs<kNarrowThreads>(p);
+    const Tile t = begin_tile(p, !p.reverse, m.j.flags);
+    XT* sx = reinterpret_cast<XT*>(m.x);
+    AT* sa = reinterpret_cast<AT*>(m.a);
+    XT* sg = reinterpret_cast<XT*>(m.g);
+    load_tile(sx, static_cast<const XT*>(p.x), p.sx, t, p.bt, p.C, p.m_x, 0.0f);
+    load_tile(sa, static_cast<const AT*>(p.a), p.sa, t, p.bt, p.G, p.m_a, 1.0f);
+    if (p.dh) load_tile(sg, static_cast<const XT*>(p.dh), p.sdh, t, p.bt, p.C, p.m_dh, 0.0f);
+    for (int i = tid; i < runs; i += kNarrowThreads) m.mk.start[i] = m.mk.finish[i] = 0;
+    if (tid == 0) m.j.flags[0] = 0;
+    __syncthreads();
+    mark_rows<RUN, kNarrowThreads>(p, m.mk, t, probe, p.dh_last, p.dh0);
+    cp_async_wait();
+    __syncthreads();
+
+    const int ch = lane * V;
+    const bool active = ch < t.nc;
+    const int col = active ? ch : 0, gate = col / p.group;
+    const unsigned starts = m.mk.start[run], finishes = p.dh_last ? m.mk.finish[run] : 0u;
+    const int l0 = run * RUN, step = p.reverse ? -1 : 1;
+    const int pr0 = p.reverse ? p.bt - 1 - l0 : l0;
+    XT* px = sx + pr0 * p.C + col;
+    const XT* pg = sg + pr0 * p.C + col;
+    AT* pa = sa + pr0 * p.G + gate;
+    const int dx = step * p.C, da = step * p.G;
+    auto gates = [&](int r, float (&av)[V]) {
+        const float a0 = to_f<AT>(pa[r * da]);
+#pragma unroll
+        for (int v = 0; v < V; ++v) av[v] = a0;
+    };
+    auto input = [&](int r, float (&xv)[V]) {
+        Pack<XT, V> q;
+        q.load(px + r * dx);
+        q.get(xv);
+    };
+    auto first = [&](int r, float (&f)[V]) {
+#pragma unroll
+        for (int v = 0; v < V; ++v)
+            f[v] = p.h0 ? p.h0[(size_t)m.mk.start_seq[pr0 + step * r] * p.C + col + v] : 0.0f;
+    };
+    auto upstream = [&](int r, float (&dv)[V]) {
+        if (p.dh) {
+            Pack<XT, V> q;
+            q.load(pg + r * dx);
+            q.get(dv);
+        } else {
+#pragma unroll
+            for (int v = 0; v < V; ++v) dv[v] = 0.0f;
+        }
+        if ((finishes >> r) & 1u) {
+            const float* q = p.dh_last + (size_t)m.mk.finish_seq[pr0 + step * r] * p.C + col;
+#pragma unroll
+            for (int v = 0; v < V; ++v) dv[v] += q[v];
+        }
+    };
+    float A[V], B[V], K[V], Ae[V], Be[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) A[v] = 1.0f, B[v] = 0.0f, K[v] = 0.0f;
+#pragma unroll 6
+    for (int r = 0; r < RUN; ++r) {
+        float av[V], uv[V];
+        gates(r, av);
+        input(r, uv);
+        if (COUPLED) rest_v<V>(uv, av, uv);
+        if ((starts >> r) & 1u) first(r, B);
+        fma_v<V>(B, av, B, uv);
+        mul_v<V>(A, A, av);
+    }
+#pragma unroll 6
+    for (int r = RUN - 1; r >= 0; --r) {
+        float av[V], dv[V];
+        gates(r, av);
+        upstream(r, dv);
+        add_v<V>(K, K, dv);
+        mul_v<V>(K, K, av);
+        if ((starts >> r) & 1u) {
+#pragma unroll
+            for (int v = 0; v < V; ++v) K[v] = 0.0f;
+        }
+    }
+    // the state in front of this run
+    float A2[V], h[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) A2[v] = A[v];
+    int fe;
+    join_runs<V>(p, m.j, true, ch, starts != 0, A2, B, fe, Ae, Be);
+    __syncthreads();
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+        h[v] = warp_carry(p, m.j, warp, ch + v, active ? p.states[(size_t)t.chunk * p.C + col + v] : 0.0f, true);
+        h[v] = fe ? Be[v] : apply(Ae[v], Be[v], h[v]);
+    }
+    __syncthreads();
+    join_runs<V>(p, m.j, false, ch, starts != 0, A, K, fe, Ae, Be);
+    __syncthreads();
+    if (join_chunks<kNarrowThreads>(p, t, m.j, false, !(m.mk.finish[runs - 1] >> (RUN - 1) & 1u))) {
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            K[v] = warp_carry(p, m.j, warp, ch + v, m.j.carry[ch + v], false);
+            K[v] = fe ? Be[v] : apply(Ae[v], Be[v], K[v]);
+        }
+        // What a gate's gradient multiplies: the state before the row (coupled:
+        // less x).  fp32 inputs hand it their place in shared memory.
+        constexpr bool kInPlace = sizeof(XT) == 4;
+        float hp[kInPlace ? 1 : RUN][V];
+#pragma unroll kInPlace ? 4 : RUN
+        for (int r = 0; r < RUN; ++r) {
+            float av[V], uv[V], q[V];
+            gates(r, av);
+            input(r, uv);
+            if ((starts >> r) & 1u) first(r, h);
+#pragma unroll
+            for (int v = 0; v < V; ++v) q[v] = COUPLED ? h[v] - uv[v] : h[v];
+            if (COUPLED) rest_v<V>(uv, av, uv);
+            fma_v<V>(h, av, h, uv);
+            if constexpr (kInPlace) {
+                if (active) Pack<XT, V>::store(px + r * dx, q);
+            } else {
+#pragma unroll
+                for (int v = 0; v < V; ++v) hp[r][v] = q[v];
+            }
+        }
+        // lanes of the row that share this lane's gate, by distance; the first of them writes its sum
+        unsigned same = 0;
+        if (p.group > V && active) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int o = lane + (1 << i);
+                if (o < lpr && o * V < t.nc && o * V / p.group == gate) same |= 1u << i;
+            }
+        }
+        const bool head = active && (ch == 0 || (ch - V) / p.group != gate);
+        const bool joined = p.group > V;
+#pragma unroll kInPlace ? 4 : RUN
+        for (int r = RUN - 1; r >= 0; --r) {
+            float av[V], dv[V], g[V], dav[V], dxv[V];
+            gates(r, av);
+            upstream(r, dv);
+            add_v<V>(g, dv, K);
+            float q[V];
+            if constexpr (kInPlace) {
+                input(r, q);
+            } else {
+#pragma unroll
+                for (int v = 0; v < V; ++v) q[v] = hp[r][v];
+            }
+            mul_v<V>(dav, g, q);
+            if (COUPLED) {
+                rest_v<V>(dxv, av, g);
+            } else {
+#pragma unroll
+                for (int v = 0; v < V; ++v) dxv[v] = g[v];
+            }
+            mul_v<V>(K, av, g);
+            if ((starts >> r) & 1u) {
+                if (p.dh0 && active) {
+                    float* q = p.dh0 + (size_t)m.mk.start_seq[pr0 + step * r] * p.C + col;
+#pragma unroll
+                    for (int v = 0; v < V; ++v) q[v] = K[v];
+                }
+#pragma unroll
+                for (int v = 0; v < V; ++v) K[v] = 0.0f;
+            }
+            float s = active ? dav[0] : 0.0f;
+#pragma unroll
+            for (int v = 1; v < V; ++v) s += dav[v];
+            if (joined) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    if ((1 << i) >= lpr) continue;
+                    const float o = __shfl_down_sync(~0u, s, 1 << i);
+                    if ((same >> i) & 1u) s += o;
+                }
+            }
+            // the gate has been read by every lane of the row that uses it
+            if (active) Pack<XT, V>::store(px + r * dx, dxv);
+            if (head) pa[r * da] = from_f<AT>(s);
+        }
+        __syncthreads();
+        store_tile(sx, static_cast<XT*>(p.dx), p.sdx, t, p.C, p.m_dx, p.zero_pad);
+        store_tile(sa, static_cast<AT*>(p.da), p.sda, t, p.G, p.m_da, p.zero_pad);
+    }
+}
+
+// Gate gradients of groups that lie in several channel blocks: the blocks'
+// parts, added in order.
+template <typename AT>
+__global__ void __launch_bounds__(kNarrowThreads) k_gate_sum(const __grid_constant__ ScanParams p) {
+    const long long total = p.rows * p.G;
+    long long lo = 0, hi = p.rows;
+    if (p.offsets) lo = seq_row(p, 0), hi = seq_row(p, p.n_seq);
+    for (long long i = (long long)blockIdx.x * kNarrowThreads + threadIdx.x; i < total;
+         i += (long long)gridDim.x * kNarrowThreads) {
+        const long long r = i / p.G;
+        const int g = (int)(i - r * p.G);
+        AT* out = static_cast<AT*>(p.da) + r * p.sda + g;
+        if (r < lo || r >= hi) {
+            if (p.zero_pad) *out = from_f<AT>(0.0f);
+            continue;
+        }
+        const int c0 = g * p.group, b0 = c0 / p.bc, b1 = (c0 + p.group - 1) / p.bc;
+        float s = 0.0f;
+        for (int b = b0; b <= b1; ++b)
+            s += p.part[((size_t)b * p.rows + r) * p.part_gates + g - b * p.bc / p.group];
+        *out = from_f<AT>(s);
+    }
+}
+
+// ---- launches of one (input, gate) type -----------------------------------
+
+template <typename AT> int launch_tail(const ScanParams& p, bool bwd, cudaStream_t s) {
+    GS_LAUNCH_CHECK();
+    if (bwd && p.partial && p.rows > 0) {
+        long long blocks = (p.rows * p.G + kNarrowThreads - 1) / kNarrowThreads;
+        if (blocks > 148 * 8) blocks = 148 * 8;
+        k_gate_sum<AT><<<(unsigned)blocks, kNarrowThreads, 0, s>>>(p); note_launch();
+        GS_LAUNCH_CHECK();
+    }
+    return GS_OK;
+}
+
+template <typename XT, typename AT, int V, bool SHARED>
+int launch_wide_fwd(const ScanParams& p, bool coupled, cudaStream_t s) {
+    auto k = coupled ? k_scan_fwd_wide<XT, AT, V, SHARED, true> : k_scan_fwd_wide<XT, AT, V, SHARED, false>;
+    const int smem = wide_smem<XT, AT, V, SHARED>(false);
+    opt_in_smem(k, smem);
+    k<<<(unsigned)p.n_chunks * (unsigned)p.n_blocks, kWideThreads, smem, s>>>(p); note_launch();
+    GS_LAUNCH_CHECK();
+    return GS_OK;
+}
+
+template <typename XT, typename AT, int V, bool SHARED>
+int launch_wide_bwd(const ScanParams& p, bool coupled, cudaStream_t s) {
+    auto k = coupled ? k_scan_bwd_wide<XT, AT, V, SHARED, true> : k_scan_bwd_wide<XT, AT, V, SHARED, false>;
+    const int smem = wide_smem<XT, AT, V, SHARED>(true);
+    opt_in_smem(k, smem);
+    k<<<(unsigned)p.n_chunks * (unsigned)p.n_blocks, kWideThreads, smem, s>>>(p); note_launch();
+    return launch_tail<AT>(p, true, s);
+}
+
+template <typename XT, typename AT, int V>
+int launch_narrow(const ScanParams& p, bool coupled, bool bwd, cudaStream_t s) {
+    const size_t smem = narrow_mem(p, sizeof(XT), sizeof(AT), bwd, nullptr, nullptr);
+    auto k = bwd ? (coupled ? k_scan_bwd_narrow<XT, AT, V, true> : k_scan_bwd_narrow<XT, AT, V, false>)
+                 : (coupled ? k_scan_fwd_narrow<XT, AT, V, true> : k_scan_fwd_narrow<XT, AT, V, false>);
+    opt_in_smem(k, 227 * 1024);
+    k<<<(unsigned)p.n_chunks * (unsigned)p.n_blocks, kNarrowThreads, smem, s>>>(p); note_launch();
+    return launch_tail<AT>(p, bwd, s);
+}
+
+template <typename XT, typename AT>
+int launch_half_type(const ScanParams& p, bool wide, int v, bool coupled, bool bwd, cudaStream_t s) {
+    if (!wide) return launch_narrow<XT, AT, 1>(p, coupled, bwd, s);
+    const bool shared = p.group > 1;
+    if (bwd) {
+        if (v == 1) return launch_wide_bwd<XT, AT, 1, false>(p, coupled, s);
+        return shared ? launch_wide_bwd<XT, AT, 2, true>(p, coupled, s)
+                      : launch_wide_bwd<XT, AT, 2, false>(p, coupled, s);
+    }
+    if (v == 1) return launch_wide_fwd<XT, AT, 1, false>(p, coupled, s);
+    if (v == 2)
+        return shared ? launch_wide_fwd<XT, AT, 2, true>(p, coupled, s)
+                      : launch_wide_fwd<XT, AT, 2, false>(p, coupled, s);
+    return shared ? launch_wide_fwd<XT, AT, 4, true>(p, coupled, s) : launch_wide_fwd<XT, AT, 4, false>(p, coupled, s);
+}
+
+}  // namespace
+}  // namespace gs
