@@ -74,7 +74,7 @@ struct Plan {
 // take at the most (as the alignment of the tensors allows).  The rows of a
 // tile, and so the states the forward leaves for the backward, do not depend
 // on it.
-bool make_plan(const gs_scan_desc* d, Plan* out, int most) {
+bool make_plan(const gs_scan_desc* d, Plan* out, int most, bool packed) {
     if (!d) return false;
     if (d->rows < 0 || d->n_seq < 0 || d->channels < 1 || d->gates < 1 || d->channels % d->gates) return false;
     if (d->dtype != GS_F32 && d->dtype != GS_BF16 && d->dtype != GS_F16) return false;
@@ -114,13 +114,23 @@ bool make_plan(const gs_scan_desc* d, Plan* out, int most) {
         p.bt = (kNarrowThreads >> p.lpr_log2) * narrow_run(q.v);
     }
     p.n_blocks = (p.C + p.bc - 1) / p.bc;
-    const long long chunks = d->rows > 0 ? (d->rows + p.bt - 1) / p.bt : 1;
-    if (chunks * p.n_blocks > 0x7fffffffll) return false;
+    // Sequences of equal length get a chain of chunks each, side by side, so
+    // that a chunk's predecessor was started long before it: where the last
+    // chunk's missing rows cost at most an eighth.
+    p.seq_len = p.n_seq > 0 ? d->rows / p.n_seq : 0;
+    const long long per_seq = (p.seq_len + p.bt - 1) / p.bt;
+    p.chain_seqs = !packed && p.n_seq > 1 && p.seq_len > 0 && d->rows % p.n_seq == 0 &&
+                           per_seq * p.bt - p.seq_len <= p.seq_len / 8
+                       ? p.n_seq : 1;
+    const long long chunks = p.chain_seqs > 1 ? per_seq : (d->rows > 0 ? (d->rows + p.bt - 1) / p.bt : 1);
+    const long long chains = (long long)p.chain_seqs * p.n_blocks;
+    if (chains > 0x7fffffffll || chunks > 0x7fffffffll / chains) return false;
     p.n_chunks = (int)chunks;
+    p.n_chains = (int)chains;
     p.partial = p.n_blocks > 1 && p.group > 1 && p.bc % p.group != 0;
     p.part_gates = p.partial ? (p.bc - 1) / p.group + 2 : 0;
     const size_t records = (size_t)p.n_chunks + (p.n_chunks + kGroup - 1) / kGroup;
-    q.rec_bytes = p.n_chunks > 1 ? records * p.n_blocks * p.bc * sizeof(ScanRecord) : 0;
+    q.rec_bytes = p.n_chunks > 1 ? records * p.n_chains * p.bc * sizeof(ScanRecord) : 0;
     q.part_bytes = p.partial ? align_up((size_t)p.n_blocks * p.rows * p.part_gates * 4, 16) : 0;
     return true;
 }
@@ -129,14 +139,16 @@ size_t plan_ws(const Plan& q) {
     return q.rec_bytes + q.part_bytes ? sizeof(WsHeader) + q.rec_bytes + q.part_bytes : 0;
 }
 
-// Workspace of the description, whatever the alignment of its tensors.
+// Workspace of the description, whatever the alignment of its tensors and the
+// way its sequences are given.
 size_t desc_ws(const gs_scan_desc* d) {
     size_t most = 0;
-    for (int v = 1; v <= kMostLanes; v *= 2) {
-        Plan q;
-        if (!make_plan(d, &q, v)) return 0;
-        most = plan_ws(q) > most ? plan_ws(q) : most;
-    }
+    for (int v = 1; v <= kMostLanes; v *= 2)
+        for (bool packed : {false, true}) {
+            Plan q;
+            if (!make_plan(d, &q, v, packed)) return 0;
+            most = plan_ws(q) > most ? plan_ws(q) : most;
+        }
     return most;
 }
 
@@ -147,7 +159,39 @@ size_t desc_ws(const gs_scan_desc* d) {
 int copy_mode(const Plan& q, const void* ptr, long long stride, int cols, int es) {
     if (!aligned(ptr, 16)) return kElem;
     if (!q.wide) return stride == cols ? kFlat : kElem;
-    return cols == q.p.C && stride * es % 16 == 0 && (long long)cols * es % 16 == 0 ? kRow16 : kElem;
+    if (cols != q.p.C || stride * es % 16 || (long long)cols * es % 16) return kElem;
+    return q.p.reverse || q.p.rows > 0x7fffffffll ? kRow16 : kTma;
+}
+
+// The TMA description of a kTma tensor; falls back to kRow16 where the driver
+// does not give one.
+void make_map(const Plan& q, int* mode, CUtensorMap* map, const void* ptr, long long stride, int dtype) {
+    using Encode = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+    static const Encode encode = [] {
+        void* fn = nullptr;
+        cudaDriverEntryPointQueryResult found;
+        if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &fn, cudaEnableDefault, &found) != cudaSuccess ||
+            found != cudaDriverEntryPointSuccess) {
+            (void)cudaGetLastError();
+            fn = nullptr;
+        }
+        return reinterpret_cast<Encode>(fn);
+    }();
+    if (*mode != kTma) return;
+    *mode = kRow16;
+    if (!encode) return;
+    const int es = elem_size(dtype);
+    const cuuint64_t dims[2] = {(cuuint64_t)q.p.C, (cuuint64_t)q.p.rows}, strides[1] = {(cuuint64_t)(stride * es)};
+    const cuuint32_t box[2] = {(cuuint32_t)q.p.bc, (cuuint32_t)kWideRun}, steps[2] = {1, 1};
+    const CUtensorMapDataType type = dtype == GS_F32    ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
+                                     : dtype == GS_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                                        : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+    if (encode(map, type, 2, const_cast<void*>(ptr), dims, strides, box, steps, CU_TENSOR_MAP_INTERLEAVE_NONE,
+               CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS)
+        *mode = kTma;
 }
 
 // Channels a lane of a wide tile may take of a tensor: as many as one aligned
@@ -161,22 +205,21 @@ void set_workspace(Plan& q, void* ws) {
     q.p.hdr = static_cast<WsHeader*>(ws);
     char* b = static_cast<char*>(ws) + sizeof(WsHeader);
     q.p.rec = reinterpret_cast<ScanRecord*>(b);
-    q.p.group_rec = q.p.rec + (size_t)q.p.n_chunks * q.p.n_blocks * q.p.bc;
+    q.p.group_rec = q.p.rec + (size_t)q.p.n_chunks * q.p.n_chains * q.p.bc;
     q.p.part = reinterpret_cast<float*>(b + q.rec_bytes);
 }
 
-int launch_typed(const Plan& q, const gs_scan_desc* d, bool bwd, cudaStream_t s) {
+int launch_typed(const Plan& q, const ScanMaps& maps, const gs_scan_desc* d, bool bwd, cudaStream_t s) {
     const bool c = (d->flags & GS_SCAN_COUPLED) != 0, g32 = d->gate_dtype == GS_F32;
-    if (d->dtype == GS_F32) return scan_launch_f32(q.p, q.wide, q.v, c, bwd, s);
-    return d->dtype == GS_BF16 ? scan_launch_bf16(q.p, g32, q.wide, q.v, c, bwd, s)
-                               : scan_launch_f16(q.p, g32, q.wide, q.v, c, bwd, s);
+    if (d->dtype == GS_F32) return scan_launch_f32(q.p, maps, q.wide, q.v, c, bwd, s);
+    return d->dtype == GS_BF16 ? scan_launch_bf16(q.p, maps, g32, q.wide, q.v, c, bwd, s)
+                               : scan_launch_f16(q.p, maps, g32, q.wide, q.v, c, bwd, s);
 }
 
 bool set_sequences(Plan& q, const long long* offsets) {
     q.p.offsets = offsets;
     if (offsets) return aligned(offsets, 8);
     if (q.p.rows % (q.p.n_seq > 0 ? q.p.n_seq : 1)) return false;
-    q.p.seq_len = q.p.n_seq > 0 ? q.p.rows / q.p.n_seq : 0;
     q.p.seq_inv = q.p.seq_len > 0 ? 1.0 / (double)q.p.seq_len : 0.0;
     return true;
 }
@@ -205,15 +248,21 @@ extern "C" size_t gs_scan_workspace_bytes(const gs_scan_desc* desc) {
 }
 
 extern "C" size_t gs_scan_states_bytes(const gs_scan_desc* desc) {
-    Plan q;
-    return make_plan(desc, &q, 1) ? (size_t)q.p.n_chunks * q.p.C * sizeof(float) : 0;
+    size_t most = 0;
+    for (bool packed : {false, true}) {
+        Plan q;
+        if (!make_plan(desc, &q, 1, packed)) return 0;
+        const size_t n = (size_t)q.p.n_chunks * q.p.chain_seqs * q.p.C * sizeof(float);
+        most = n > most ? n : most;
+    }
+    return most;
 }
 
 extern "C" int gs_scan_fwd(const gs_scan_desc* desc, const void* a, const void* x, const float* h0,
                            const long long* seq_offsets, void* h, float* h_last, float* states, void* ws,
                            size_t ws_bytes, void* stream) {
     Plan q;
-    if (!make_plan(desc, &q, 1) || !set_sequences(q, seq_offsets)) return GS_ERR_INVALID_ARG;
+    if (!make_plan(desc, &q, 1, seq_offsets != nullptr) || !set_sequences(q, seq_offsets)) return GS_ERR_INVALID_ARG;
     if (desc->n_seq == 0) return GS_OK;
     const int xs = elem_size(desc->dtype), as = elem_size(desc->gate_dtype);
     if (desc->rows > 0 && (!a || !x || !aligned(a, as) || !aligned(x, xs))) return GS_ERR_INVALID_ARG;
@@ -224,14 +273,17 @@ extern "C" int gs_scan_fwd(const gs_scan_desc* desc, const void* a, const void* 
     int most = lanes_ok(x, desc->stride_x, xs, most_lanes(desc->dtype, false));
     if (h) most = lanes_ok(h, desc->stride_h, xs, most);
     if (desc->gates == desc->channels) most = lanes_ok(a, desc->stride_a, as, most);
-    if (!make_plan(desc, &q, most) || !set_sequences(q, seq_offsets)) return GS_ERR_INVALID_ARG;
+    if (!make_plan(desc, &q, most, seq_offsets != nullptr) || !set_sequences(q, seq_offsets)) return GS_ERR_INVALID_ARG;
     ScanParams& p = q.p;
     p.a = a, p.x = x, p.h0 = h0, p.h = h, p.h_last = h_last, p.states = states;
     p.m_a = copy_mode(q, a, p.sa, p.G, as);
     p.m_x = copy_mode(q, x, p.sx, p.C, xs);
     p.m_h = copy_mode(q, h, p.sh, p.C, xs);
     if (need) set_workspace(q, ws);
-    return launch_typed(q, desc, false, (cudaStream_t)stream);
+    ScanMaps maps{};
+    make_map(q, &p.m_a, &maps.a, a, p.sa, desc->gate_dtype);
+    make_map(q, &p.m_x, &maps.x, x, p.sx, desc->dtype);
+    return launch_typed(q, maps, desc, false, (cudaStream_t)stream);
 }
 
 extern "C" int gs_scan_bwd(const gs_scan_desc* desc, const void* a, const void* x, const float* h0,
@@ -239,7 +291,7 @@ extern "C" int gs_scan_bwd(const gs_scan_desc* desc, const void* a, const void* 
                            const float* dL_dh_last, void* dL_da, void* dL_dx, float* dL_dh0, void* ws,
                            size_t ws_bytes, void* stream) {
     Plan q;
-    if (!make_plan(desc, &q, 1) || !set_sequences(q, seq_offsets)) return GS_ERR_INVALID_ARG;
+    if (!make_plan(desc, &q, 1, seq_offsets != nullptr) || !set_sequences(q, seq_offsets)) return GS_ERR_INVALID_ARG;
     if (desc->n_seq == 0) return GS_OK;
     const int xs = elem_size(desc->dtype), as = elem_size(desc->gate_dtype);
     if (desc->rows > 0 && (!a || !x || !dL_da || !dL_dx || !states || !aligned(a, as) || !aligned(x, xs) ||
@@ -257,7 +309,7 @@ extern "C" int gs_scan_bwd(const gs_scan_desc* desc, const void* a, const void* 
         most = lanes_ok(a, desc->stride_a, as, most);
         most = lanes_ok(dL_da, desc->stride_da, as, most);
     }
-    if (!make_plan(desc, &q, most) || !set_sequences(q, seq_offsets)) return GS_ERR_INVALID_ARG;
+    if (!make_plan(desc, &q, most, seq_offsets != nullptr) || !set_sequences(q, seq_offsets)) return GS_ERR_INVALID_ARG;
     if (desc->rows == 0 && !dL_dh0) return GS_OK;
     ScanParams& p = q.p;
     p.a = a, p.x = x, p.h0 = h0, p.states = const_cast<float*>(states);
@@ -268,13 +320,17 @@ extern "C" int gs_scan_bwd(const gs_scan_desc* desc, const void* a, const void* 
     p.m_da = copy_mode(q, dL_da, p.sda, p.G, as);
     p.m_dx = copy_mode(q, dL_dx, p.sdx, p.C, xs);
     if (need) set_workspace(q, ws);
-    return launch_typed(q, desc, true, (cudaStream_t)stream);
+    ScanMaps maps{};
+    make_map(q, &p.m_a, &maps.a, a, p.sa, desc->gate_dtype);
+    make_map(q, &p.m_x, &maps.x, x, p.sx, desc->dtype);
+    make_map(q, &p.m_dh, &maps.d, dL_dh, p.sdh, desc->dtype);
+    return launch_typed(q, maps, desc, true, (cudaStream_t)stream);
 }
 
 extern "C" int gs_scan_step(const gs_scan_desc* desc, const void* a, const void* x, const float* state,
                             float* state_out, void* h, void* stream) {
     Plan q;
-    if (!make_plan(desc, &q, 1) || desc->n_seq != desc->rows) return GS_ERR_INVALID_ARG;
+    if (!make_plan(desc, &q, 1, false) || desc->n_seq != desc->rows) return GS_ERR_INVALID_ARG;
     if (desc->rows == 0) return GS_OK;
     const int xs = elem_size(desc->dtype), as = elem_size(desc->gate_dtype);
     if (!a || !x || !state || !state_out || !aligned(a, as) || !aligned(x, xs) || !aligned(state, 4) ||

@@ -11,6 +11,7 @@
 
 #include <climits>
 
+#include <cuda.h>  // CUtensorMap
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -33,17 +34,15 @@ constexpr int kWideThreads = 128, kNarrowThreads = 256;
 #ifndef BMB
 #define BMB 4
 #endif
-#ifndef NGRP
-#define NGRP 4
-#endif
 constexpr int kWideRun = WRUN;
 constexpr int narrow_run(int v) { return v >= 3 ? 11 : 17; }
 constexpr unsigned kSpinLimit = 1u << 20;
 
 // How a tile's rows are moved: in 16-byte pieces of the whole tile (narrow
-// tiles whose rows are one contiguous range) or of each row (wide tiles), or
-// element by element.
-enum CopyMode { kFlat = 0, kRow16 = 1, kElem = 2 };
+// tiles whose rows are one contiguous range); wide tiles by TMA, a run at a
+// time, or (scans in reverse, whose runs lie the other way) in 16-byte pieces
+// of each row; else element by element.
+enum CopyMode { kFlat = 0, kTma = 1, kRow16 = 2, kElem = 3 };
 
 struct ScanRecord {  // 16 bytes, published with one 128-bit store
     float A, B;
@@ -58,7 +57,9 @@ struct ScanParams {
     const long long* offsets;  // NULL: n_seq sequences of seq_len rows
     long long sa, sx, sh, sda, sdx, sdh;
     int C, G, group;           // group = C / G channels per gate
-    int n_seq, n_chunks, n_blocks;
+    int n_seq, n_blocks;       // sequences; blocks of channels
+    int n_chunks, n_chains;    // chunks of a chain; chains of chunks whose carries travel apart
+    int chain_seqs;            // sequences with chains of their own (equal lengths), or 1: one chain over all rows
     int lpr_log2;              // narrow: lanes per row, as a power of two
     int bc, bt;                // channels of a block, rows of a tile
     int reverse, zero_pad, partial, part_gates;
@@ -71,11 +72,17 @@ struct ScanParams {
     ScanRecord *rec, *group_rec;  // per chunk, and per kGroup chunks
 };
 
+// TMA descriptions of a, x and dL/dh as matrices of rows x channels with boxes
+// of one run (kWideRun rows x bc channels); filled where the mode is kTma.
+struct ScanMaps {
+    CUtensorMap a, x, d;
+};
+
 // Launches the scan (bwd: its adjoint) of one element type; `wide` and `v`
 // as chosen by the plan.
-int scan_launch_f32(const ScanParams& p, bool wide, int v, bool coupled, bool bwd, cudaStream_t s);
-int scan_launch_bf16(const ScanParams& p, bool gate_f32, bool wide, int v, bool coupled, bool bwd, cudaStream_t s);
-int scan_launch_f16(const ScanParams& p, bool gate_f32, bool wide, int v, bool coupled, bool bwd, cudaStream_t s);
+int scan_launch_f32(const ScanParams& p, const ScanMaps& maps, bool wide, int v, bool coupled, bool bwd, cudaStream_t s);
+int scan_launch_bf16(const ScanParams& p, const ScanMaps& maps, bool gate_f32, bool wide, int v, bool coupled, bool bwd, cudaStream_t s);
+int scan_launch_f16(const ScanParams& p, const ScanMaps& maps, bool gate_f32, bool wide, int v, bool coupled, bool bwd, cudaStream_t s);
 
 namespace {
 
@@ -261,6 +268,41 @@ __device__ __forceinline__ void cp_async16(void* smem, const void* gmem) {
 }
 __device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
+// TMA loads into shared memory and the barrier that counts their bytes.  A
+// tile starts at a multiple of 32 channels, so on a 16-byte boundary.
+__device__ __forceinline__ void barrier_init(unsigned long long* bar) {
+    const unsigned b = (unsigned)__cvta_generic_to_shared(bar);
+    asm volatile("mbarrier.init.shared.b64 [%0], 1;" ::"r"(b) : "memory");
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+}
+__device__ __forceinline__ void barrier_expect(unsigned long long* bar, unsigned bytes) {
+    const unsigned b = (unsigned)__cvta_generic_to_shared(bar);
+    asm volatile("mbarrier.arrive.expect_tx.shared.b64 _, [%0], %1;" ::"r"(b), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void tile_load(void* smem, const CUtensorMap* map, int col, int row,
+                                          unsigned long long* bar) {
+    const unsigned d = (unsigned)__cvta_generic_to_shared(smem), b = (unsigned)__cvta_generic_to_shared(bar);
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(
+            d),
+        "l"(map), "r"(col), "r"(row), "r"(b)
+        : "memory");
+}
+// Waits for the barrier's first phase; false when the wait ran out.
+__device__ __forceinline__ bool barrier_wait(unsigned long long* bar) {
+    const unsigned b = (unsigned)__cvta_generic_to_shared(bar);
+    for (unsigned spin = 0; spin < kSpinLimit; ++spin) {
+        unsigned done;
+        asm volatile(
+            "{ .reg .pred q; mbarrier.try_wait.parity.shared.b64 q, [%1], 0; selp.u32 %0, 1, 0, q; }"
+            : "=r"(done)
+            : "r"(b)
+            : "memory");
+        if (done) return true;
+    }
+    return false;
+}
+
 // Row offset of sequence j (j = n_seq: the end), clamped to the tensor so
 // that bad offsets can give wrong values but no access out of range.
 __device__ __forceinline__ long long seq_row(const ScanParams& p, long long j) {
@@ -280,9 +322,10 @@ struct Marks {
 
 // Which tile this block works on, and where it lies.
 struct Tile {
-    int k;            // chunk in the order the carry travels
-    int chunk;        // chunk in row order
-    int cb, c0, nc;   // channel block
+    int k, chain;     // chunk in the order the carry travels, and its chain
+    long long chunk;  // chunk in row order
+    int c0, nc;       // channel block
+    bool last_chunk;  // of all rows
     int n;            // rows of this tile
     int lo, hi;       // local range of the rows that belong to sequences
     long long r0;
@@ -310,7 +353,6 @@ template <int RUN, int NT>
 __device__ __forceinline__ void mark_rows(const ScanParams& p, const Marks& mk, const Tile& t, SeqProbe q,
                                           const float* from, float* to) {
     const long long end = t.r0 + p.bt;
-    const bool last_chunk = t.chunk == p.n_chunks - 1;
     // lo: no offset in front of entry lo reaches the tile, and the first that does is less than NT further
     long long lo = 0;
     if (p.offsets) {
@@ -337,7 +379,7 @@ __device__ __forceinline__ void mark_rows(const ScanParams& p, const Marks& mk, 
         const long long next = j < p.n_seq ? seq_row(p, j + 1) : v, prev = j > 0 ? seq_row(p, j - 1) : v;
         if (v > end) break;
         if (v < t.r0) continue;
-        if (j < p.n_seq && (v < end || last_chunk)) {
+        if (j < p.n_seq && (v < end || t.last_chunk)) {
             if (next > v) {
                 if (v < t.r0 + t.n) {
                     const int pr = (int)(v - t.r0);
@@ -369,22 +411,63 @@ template <int V> __device__ __forceinline__ void get_words(const float* p, float
 struct Joins {
     float *wA, *wB;   // [warps][bc] each warp's composite
     float *carry;     // [bc] what comes in from the chunks before
-    int *flags;       // [0] a wait ran out, [1] ticket, [2] epoch
+    int *flags;       // [0] a wait ran out, [1] ticket, [2] epoch, [4..6] Ahead
     int *wf;          // [warps] whether the warp's composite absorbs
 };
 
-// Waits for a record of this call.  False when the wait ran out.
-__device__ __forceinline__ bool await(const ScanParams& p, const ScanRecord* q, unsigned tag, ScanRecord& r,
-                                      unsigned& spin) {
-    while ((r.tag | 1u) != (tag | 1u)) {
+// Reads a record again.  False when the wait ran out.
+__device__ __forceinline__ bool again(const ScanParams& p, const ScanRecord* q, ScanRecord& r, unsigned& spin) {
+    if (++spin > kSpinLimit || ((spin & 1023u) == 0 && *reinterpret_cast<volatile unsigned*>(&p.hdr->status))) {
+        raise_status(p.hdr, GS_ERR_TIMEOUT);
+        return false;
+    }
+    r = poll(q);
+    return true;
+}
+
+// What is known of the chunks before a tile's: how many chunks of its group
+// count (up to the nearest whose state is known: then `stop`), and the nearest
+// group whose state is known (-1: none yet).
+struct Ahead {
+    int far, stop, group;
+};
+
+// Warp 0 looks at one channel's records, the chunks of the group and kLookGroups
+// groups before it in one round trip, until they are there (`groups`: until a
+// group's state is).  False when the wait ran out.  (All channels looking by
+// themselves, as often as it takes, took most of the L2's bandwidth: 65,536 x
+// 2048 bf16 forward 189 us against 131 us without any joins.)
+constexpr int kLookGroups = 24;
+
+__device__ __forceinline__ bool look_ahead(const ScanParams& p, const Tile& t, const ScanRecord* rec,
+                                           const ScanRecord* grec, size_t stride, bool groups, Ahead& r) {
+    const int lane = threadIdx.x & 31, g = t.k / kGroup, before = t.k % kGroup;
+    const bool is_chunk = lane < kGroup - 1, is_group = lane >= 8;
+    const bool mine = is_chunk ? lane < before : (is_group && lane - 8 < g);
+    const ScanRecord* q = is_chunk ? rec - (ptrdiff_t)(lane + 1) * stride : grec - (ptrdiff_t)(lane - 7) * stride;
+    unsigned spin = 0, tag = 0;
+    while (true) {
+        if (mine && (tag | 1u) != t.tag + 1u) tag = poll(q).tag;
+        else if (mine && is_group && !(tag & 1u)) tag = poll(q).tag;
+        const bool there = mine && (tag | 1u) == t.tag + 1u, final = there && (tag & 1u);
+        const unsigned m_there = __ballot_sync(~0u, there), m_final = __ballot_sync(~0u, final);
+        // chunks: all of them, or those nearer than a known state
+        const unsigned c_final = m_final & 0x7fu, c_gap = ~m_there & ((1u << before) - 1u);
+        const int c_first = c_final ? __ffs(c_final) - 1 : before;
+        const bool c_ok = (c_gap & ((1u << c_first) - 1u)) == 0;
+        r.stop = c_final != 0;
+        r.far = c_final ? c_first + 1 : before;
+        // groups: a known state, and every composite nearer than it
+        const unsigned g_final = m_final >> 8, g_there = m_there >> 8;
+        const int g_first = g_final ? __ffs(g_final) - 1 : -1;
+        r.group = g_final && (~g_there & ((1u << g_first) - 1u)) == 0 ? g_first : -1;
+        if (c_ok && (!groups || r.stop || r.group >= 0)) return true;
         if (++spin > kSpinLimit || ((spin & 1023u) == 0 && *reinterpret_cast<volatile unsigned*>(&p.hdr->status))) {
-            raise_status(p.hdr, GS_ERR_TIMEOUT);
+            if (lane == 0) raise_status(p.hdr, GS_ERR_TIMEOUT);
             return false;
         }
-        __nanosleep(20);
-        r = poll(q);
+        __nanosleep(40);
     }
-    return true;
 }
 
 // Joins the tile to the chunks before it, given every warp's composite in
@@ -393,15 +476,12 @@ __device__ __forceinline__ bool await(const ScanParams& p, const ScanRecord* q, 
 // first row in travel order starts a sequence, or finishes one when the
 // carry travels down).  False when a wait ran out.
 //
-// One thread per channel.  A chunk publishes its composite at once.  Chunks
-// form groups of kGroup: the last one of a group publishes the group's
-// composite, and the state after the group when it knows it.  A chunk folds
-// the chunks of its own group before it, and looks back over whole groups to
-// the nearest whose state is known, kLookGroups of them in one round trip.
-// Every value is a fixed expression of the chunks' composites, whichever
-// groups happened to be finished, so equal inputs give equal bits.
-constexpr int kLookGroups = NGRP;
-
+// A chunk publishes its composite at once.  Chunks form groups of kGroup: the
+// last one of a group publishes the group's composite, and the state after
+// the group when it knows it.  A chunk folds the chunks of its own group
+// before it, and looks back over whole groups to the nearest whose state is
+// known.  Every value is a fixed expression of the chunks' composites,
+// whichever groups happened to be finished, so equal inputs give equal bits.
 template <int NT>
 __device__ __forceinline__ bool join_chunks(const ScanParams& p, const Tile& t, const Joins& m, bool up, bool needed) {
     constexpr int kWarps = NT / 32;
@@ -411,87 +491,82 @@ __device__ __forceinline__ bool join_chunks(const ScanParams& p, const Tile& t, 
         __syncthreads();
         return true;
     }
-    if (tid < bc) {
-        float A = 1.0f, B = 0.0f, carry = 0.0f;
-        bool known = t.k == 0;  // B is the state after this chunk, whatever comes in
+    const size_t stride = (size_t)p.n_chains * bc, at = (size_t)t.chain * bc;
+    const int g = t.k / kGroup;
+    ScanRecord *rec = p.rec + (size_t)t.k * stride + at, *grec = p.group_rec + (size_t)g * stride + at;
+    const bool closes = t.k % kGroup == kGroup - 1, mine = tid < bc;
+    bool known = t.k == 0;  // the state after this chunk is B, whatever comes in
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) known |= m.wf[w] != 0;
+    float A = 1.0f, B = 0.0f, carry = 0.0f;
+    if (mine) {
 #pragma unroll
         for (int i = 0; i < kWarps; ++i) {
             const int w = up ? i : kWarps - 1 - i;
             const float wa = m.wA[w * bc + tid], wb = m.wB[w * bc + tid];
-            if (m.wf[w]) B = wb, known = true;
-            else B = apply(wa, wb, B), A *= wa;
+            B = m.wf[w] ? wb : apply(wa, wb, B);
+            A *= wa;
         }
-        const size_t stride = (size_t)p.n_blocks * bc, at = (size_t)t.cb * bc + tid;
-        ScanRecord* rec = p.rec + (size_t)t.k * stride + at;
-        publish(rec, known ? 0.0f : A, B, t.tag | (known ? 1u : 0u));
-        const int g = t.k / kGroup, before = t.k % kGroup;
-        ScanRecord* grec = p.group_rec + (size_t)g * stride + at;
-        const bool closes = before == kGroup - 1;
-        if (known && closes) publish(grec, 0.0f, B, t.tag | 1u);
-        if (t.k > 0 && (needed || (closes && !known))) {
-            ScanRecord r[kGroup - 1], q[kLookGroups];
+        publish(rec + tid, known ? 0.0f : A, B, t.tag | (known ? 1u : 0u));
+        if (known && closes) publish(grec + tid, 0.0f, B, t.tag | 1u);
+    }
+    if (t.k > 0 && (needed || (closes && !known))) {
+        Ahead* seen = reinterpret_cast<Ahead*>(m.flags + 4);
+        auto look = [&](bool groups) {
+            if (tid < 32) {
+                Ahead r;
+                const bool ok = look_ahead(p, t, rec, grec, stride, groups, r);
+                if (tid == 0) {
+                    *seen = r;
+                    if (!ok) m.flags[0] = 1;
+                }
+            }
+            __syncthreads();
+        };
+        look(!closes || known);
+        Ahead r = *seen;
+        bool ok = m.flags[0] == 0;
+        float PA = 1.0f, PB = 0.0f, S = 0.0f;
+        unsigned spin = 0;
+        // the state after group g - 1, from that of the nearest group that has one
+        auto state = [&]() {
+            for (int u = r.group; u >= 0 && ok; --u) {
+                const ScanRecord* q = grec + tid - (ptrdiff_t)(u + 1) * stride;
+                ScanRecord v = poll(q);
+                while (ok && !(v.tag == t.tag + 1u || (u < r.group && v.tag == t.tag))) ok = again(p, q, v, spin);
+                S = v.tag & 1u ? v.B : apply(v.A, v.B, S);
+            }
+        };
+        if (mine && ok) {
+            ScanRecord v[kGroup - 1];
 #pragma unroll
             for (int u = 0; u < kGroup - 1; ++u)
-                if (u < before) r[u] = poll(rec - (u + 1) * stride);
-#pragma unroll
-            for (int u = 0; u < kLookGroups; ++u)
-                if (u < g) q[u] = poll(grec - (u + 1) * stride);
-            // the chunks of this group before this one
-            unsigned spin = 0;
-            bool ok = true, stop = false;
-            int far = 0;  // how many of them count: up to the nearest whose state is known
-#pragma unroll
-            for (int u = 0; u < kGroup - 1; ++u) {
-                if (u >= before || stop || !ok) continue;
-                ok = await(p, rec - (u + 1) * stride, t.tag, r[u], spin);
-                stop = r[u].tag & 1u;
-                far = u + 1;
-            }
-            float PA = 1.0f, PB = 0.0f;
+                if (u < r.far) v[u] = poll(rec + tid - (ptrdiff_t)(u + 1) * stride);
+            if (!r.stop) state();
 #pragma unroll
             for (int u = kGroup - 2; u >= 0; --u) {
-                if (u >= far) continue;
-                PB = apply(r[u].A, r[u].B, PB);
-                PA *= r[u].A;
+                if (u >= r.far) continue;
+                while (ok && (v[u].tag | 1u) != t.tag + 1u)
+                    ok = again(p, rec + tid - (ptrdiff_t)(u + 1) * stride, v[u], spin);
+                PB = apply(v[u].A, v[u].B, PB);
+                PA *= v[u].A;
             }
-            const float GA = PA * A, GB = apply(A, B, PB);
-            if (ok && closes && !known) publish(grec, GA, GB, t.tag | (stop ? 1u : 0u));
-            carry = PB;
-            if (ok && !stop) {
-                // whole groups: wait until one of the window has its state, and those nearer their composites
-                int last = -1;
-                while (ok && last < 0) {
-                    bool gap = false;
-#pragma unroll
-                    for (int u = 0; u < kLookGroups; ++u) {
-                        if (u >= g || last >= 0 || gap) continue;
-                        if ((q[u].tag | 1u) != (t.tag | 1u)) gap = true;
-                        else if (q[u].tag & 1u) last = u;
-                    }
-                    if (last >= 0) break;
-                    if (++spin > kSpinLimit ||
-                        ((spin & 1023u) == 0 && *reinterpret_cast<volatile unsigned*>(&p.hdr->status))) {
-                        raise_status(p.hdr, GS_ERR_TIMEOUT);
-                        ok = false;
-                    }
-                    __nanosleep(20);
-#pragma unroll
-                    for (int u = 0; u < kLookGroups; ++u)
-                        if (u < g) q[u] = poll(grec - (u + 1) * stride);
-                }
-                float S = 0.0f;
-#pragma unroll
-                for (int u = kLookGroups - 1; u >= 0; --u) {
-                    if (u == last) S = q[u].B;
-                    else if (u < last) S = apply(q[u].A, q[u].B, S);
-                }
-                carry = apply(PA, PB, S);
-                if (ok && closes && !known) publish(grec, 0.0f, apply(GA, GB, S), t.tag | 1u);
-            }
-            if (!ok) m.flags[0] = 1;
         }
-        m.carry[tid] = carry;
+        const float GA = PA * A, GB = apply(A, B, PB);
+        const bool late = !r.stop && r.group < 0;  // (a group's last chunk) its own group first, then those before
+        if (closes && !known && mine && ok && (r.stop || late)) publish(grec + tid, GA, GB, t.tag | (r.stop ? 1u : 0u));
+        if (late) {
+            __syncthreads();  // everyone has read *seen
+            look(true);
+            r = *seen;
+            ok = ok && m.flags[0] == 0;
+            if (mine && ok) state();
+        }
+        carry = r.stop ? PB : apply(PA, PB, S);
+        if (closes && !known && !r.stop && mine && ok) publish(grec + tid, 0.0f, apply(GA, GB, S), t.tag | 1u);
+        if (!ok) m.flags[0] = 1;
     }
+    if (mine) m.carry[tid] = carry;
     __syncthreads();
     return m.flags[0] == 0;
 }
@@ -518,13 +593,16 @@ __device__ __forceinline__ Tile begin_tile(const ScanParams& p, bool descending,
         epoch = (unsigned)flags[2];
     }
     t.tag = 2u * (epoch + 1u);
-    t.k = (int)(id / (unsigned)p.n_blocks);
-    t.cb = (int)(id - (unsigned)t.k * (unsigned)p.n_blocks);
-    t.chunk = descending ? p.n_chunks - 1 - t.k : t.k;
-    t.c0 = t.cb * p.bc;
+    t.k = (int)(id / (unsigned)p.n_chains);
+    t.chain = (int)(id - (unsigned)t.k * (unsigned)p.n_chains);
+    const int seq = p.chain_seqs > 1 ? t.chain / p.n_blocks : 0, k = descending ? p.n_chunks - 1 - t.k : t.k;
+    const long long rows = p.chain_seqs > 1 ? p.seq_len : p.rows;  // of the chain
+    t.chunk = (long long)seq * p.n_chunks + k;
+    t.last_chunk = t.chunk == (long long)p.chain_seqs * p.n_chunks - 1;
+    t.c0 = (t.chain - seq * p.n_blocks) * p.bc;
     t.nc = min(p.bc, p.C - t.c0);
-    t.r0 = (long long)t.chunk * p.bt;
-    t.n = (int)max(0ll, min((long long)p.bt, p.rows - t.r0));
+    t.r0 = seq * p.seq_len * (p.chain_seqs > 1) + (long long)k * p.bt;
+    t.n = (int)max(0ll, min((long long)p.bt, rows - (long long)k * p.bt));
     t.lo = (int)min(max(first - t.r0, 0ll), (long long)t.n);
     t.hi = (int)min(max(end - t.r0, (long long)t.lo), (long long)t.n);
     return t;
@@ -540,27 +618,32 @@ template <int V> struct WideShared {
     float wA[kWideWarps * 32 * V], wB[kWideWarps * 32 * V], carry[32 * V];
     unsigned start[kWideWarps], finish[kWideWarps];
     int start_seq[kWideRows], finish_seq[kWideRows];
-    int flags[4], wf[kWideWarps];
+    int flags[8], wf[kWideWarps];
+    unsigned long long bar[kWideWarps];
     __device__ Marks marks() { return {start, finish, start_seq, finish_seq}; }
     __device__ Joins joins() { return {wA, wB, carry, flags, wf}; }
 };
 
 // Rows whose loads from shared memory are in flight together; left to itself
 // the compiler raises all rows' loads to the top and spills.
-constexpr int kStep = 4;
+#ifndef KSTEP
+#define KSTEP 4
+#endif
+constexpr int kStep = KSTEP;
 __device__ __forceinline__ void step_fence(int r) {
     if (r % kStep == 0) asm volatile("" ::: "memory");
 }
 
 // One tensor's rows of a warp's run in shared memory, copied there
-// asynchronously by the warp: in 16-byte pieces that bypass L1 where the rows
-// allow it (a tile's shared memory leaves L1 too small for the loads in
-// flight), else each lane its own elements.
+// asynchronously by the warp: by TMA where the rows allow it (one instruction
+// a run, past the load pipeline, where the tickets and records of other tiles
+// would queue behind it), in 16-byte pieces, or each lane its own elements.
 template <typename T, int V> struct Column {
     T* run;  // first row of the run
     T* s;    // this lane's element of it
     static constexpr int kRow = 32 * V;
-    static constexpr int kBytes = kWideRows * kRow * (int)sizeof(T);
+    static constexpr int kRunBytes = kWideRun * kRow * (int)sizeof(T);
+    static constexpr int kBytes = (kWideWarps * kRunBytes + 127) / 128 * 128;
     __device__ __forceinline__ Column(char* base, int warp, int lane)
         : run(reinterpret_cast<T*>(base) + warp * kWideRun * kRow), s(run + lane * V) {}
     __device__ __forceinline__ void copy(int r, const T* g) {
@@ -590,8 +673,9 @@ template <typename T, int V> struct Column {
             }
         }
     }
-    // All rows of the run in 16-byte pieces; g: first of the block's `cols`
-    // columns.
+    // All rows of the run in 16-byte pieces, past L1 (a tile's shared memory
+    // leaves it too small for the loads in flight); g: first of the block's
+    // `cols` columns.
     __device__ __forceinline__ void load16(const T* g, long long step, int cols) {
         constexpr int kPer = 16 / (int)sizeof(T), kLanes = kRow / kPer, kRows = 32 / kLanes;
         const int lane = threadIdx.x & 31, piece = lane % kLanes, r0 = lane / kLanes;
@@ -610,15 +694,29 @@ template <typename T, int V> struct Column {
     __device__ __forceinline__ void put(int r, const float (&f)[V]) { Pack<T, V>::store(s + r * kRow, f); }
 };
 
-// Gates: V of them, or one for all V channels.
+// Gates: V to a lane; or, shared, one for all V channels of a lane, kept once
+// per row where it is the same for the whole warp.
 template <typename AT, int V, bool SHARED> struct Gates : Column<AT, SHARED ? 1 : V> {
-    using Column<AT, SHARED ? 1 : V>::Column;
+    using Base = Column<AT, SHARED ? 1 : V>;
+    using Base::Base;
+    const AT* at;  // SHARED: this lane's gate of the first row
+    int pitch;
+    // One gate a row: lane r brings row r's.
+    __device__ __forceinline__ void load_rows(const AT* g, long long step, unsigned live) {
+        const int lane = threadIdx.x & 31;
+        at = this->run, pitch = 1;
+        if (lane < kWideRun) this->run[lane] = (live >> lane) & 1u ? g[lane * step] : from_f<AT>(1.0f);
+        __syncwarp();
+    }
+    __device__ __forceinline__ void load_lanes(const AT* g, long long step, unsigned live) {
+        at = this->s, pitch = Base::kRow;
+        this->load(g, step, live, 1.0f);
+    }
     __device__ __forceinline__ void wide(int r, float (&f)[V]) const {
         if constexpr (SHARED) {
-            float s[1];
-            this->get(r, s);
+            const float a = to_f<AT>(at[r * pitch]);
 #pragma unroll
-            for (int v = 0; v < V; ++v) f[v] = s[0];
+            for (int v = 0; v < V; ++v) f[v] = a;
         } else {
             this->get(r, f);
         }
@@ -627,7 +725,7 @@ template <typename AT, int V, bool SHARED> struct Gates : Column<AT, SHARED ? 1 
 
 template <typename XT, typename AT, int V, bool SHARED>
 constexpr int wide_smem(bool bwd) {
-    return (int)(sizeof(WideShared<V>) + 15) / 16 * 16 + Gates<AT, V, SHARED>::kBytes +
+    return (int)(sizeof(WideShared<V>) + 127) / 128 * 128 + Gates<AT, V, SHARED>::kBytes +
            Column<XT, V>::kBytes * (bwd ? 2 : 1);
 }
 
@@ -659,10 +757,11 @@ __device__ __forceinline__ void wide_carry(const WideShared<V>& sm, int warp, in
 }
 
 template <typename XT, typename AT, int V, bool SHARED, bool COUPLED>
-__global__ void __launch_bounds__(kWideThreads, FMB) k_scan_fwd_wide(const __grid_constant__ ScanParams p) {
-    extern __shared__ __align__(16) char smem[];
+__global__ void __launch_bounds__(kWideThreads, FMB) k_scan_fwd_wide(const __grid_constant__ ScanParams p,
+                                                                   const __grid_constant__ ScanMaps maps) {
+    extern __shared__ __align__(128) char smem[];
     WideShared<V>& sm = *reinterpret_cast<WideShared<V>*>(smem);
-    char* data = smem + (sizeof(WideShared<V>) + 15) / 16 * 16;
+    char* data = smem + (sizeof(WideShared<V>) + 127) / 128 * 128;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const Joins m = sm.joins();
     const SeqProbe probe = probe_seqs<kWideThreads>(p);
@@ -681,14 +780,36 @@ __global__ void __launch_bounds__(kWideThreads, FMB) k_scan_fwd_wide(const __gri
     Column<XT, V> xs(data + Gates<AT, V, SHARED>::kBytes, warp, lane);
     const AT* ga = static_cast<const AT*>(p.a) + row0 * p.sa;
     const XT* gx = static_cast<const XT*>(p.x) + row0 * p.sx;
-    if (!SHARED && p.m_a == kRow16 && live == kAllRows) as.load16(ga + t.c0, dir * p.sa, t.nc);
-    else as.load(ga + (p.group == 1 ? col : col / p.group), dir * p.sa, live, 1.0f);
-    if (p.m_x == kRow16 && live == kAllRows) xs.load16(gx + t.c0, dir * p.sx, t.nc);
-    else xs.load(gx + col, dir * p.sx, live, 0.0f);
+    const bool full = live == kAllRows;
+    const bool tile_a = !SHARED && full && p.m_a == kTma, tile_x = full && p.m_x == kTma;
+    unsigned long long* bar = &sm.bar[warp];
+    if (lane == 0) {
+        barrier_init(bar);
+        barrier_expect(bar, tile_a * as.kRunBytes + tile_x * xs.kRunBytes);
+        if (tile_x) tile_load(xs.run, &maps.x, t.c0, (int)row0, bar);
+        if (tile_a) tile_load(as.run, &maps.a, t.c0, (int)row0, bar);
+    }
+    __syncwarp();
+    if constexpr (SHARED) {
+        if (t.c0 / p.group == (t.c0 + t.nc - 1) / p.group) as.load_rows(ga + t.c0 / p.group, dir * p.sa, live);
+        else as.load_lanes(ga + col / p.group, dir * p.sa, live);
+    } else if (!tile_a) {
+        if (full && p.m_a == kRow16) as.load16(ga + t.c0, dir * p.sa, t.nc);
+        else as.load(ga + (p.group == 1 ? col : col / p.group), dir * p.sa, live, 1.0f);
+    }
+    if (!tile_x) {
+        if (full && p.m_x == kRow16) xs.load16(gx + t.c0, dir * p.sx, t.nc);
+        else xs.load(gx + col, dir * p.sx, live, 0.0f);
+    }
     __syncthreads();
     mark_rows<kWideRun, kWideThreads>(p, sm.marks(), t, probe, p.h0, p.h_last);
     cp_async_wait();
+    if (!barrier_wait(bar) && !barrier_wait(bar)) sm.flags[0] = 1;
     __syncthreads();
+    if (sm.flags[0]) {  // cannot happen while the copies' addresses are valid
+        if (tid == 0 && p.hdr) raise_status(p.hdr, GS_ERR_TIMEOUT);
+        return;
+    }
     const unsigned starts = sm.start[warp], finishes = sm.finish[warp];
     const bool plain = (starts | finishes) == 0 && live == kAllRows;
 
@@ -791,10 +912,11 @@ __device__ __forceinline__ void sum_rows(float (&s)[8], int bits, int lane) {
 }
 
 template <typename XT, typename AT, int V, bool SHARED, bool COUPLED>
-__global__ void __launch_bounds__(kWideThreads, BMB) k_scan_bwd_wide(const __grid_constant__ ScanParams p) {
-    extern __shared__ __align__(16) char smem[];
+__global__ void __launch_bounds__(kWideThreads, BMB) k_scan_bwd_wide(const __grid_constant__ ScanParams p,
+                                                                   const __grid_constant__ ScanMaps maps) {
+    extern __shared__ __align__(128) char smem[];
     WideShared<V>& sm = *reinterpret_cast<WideShared<V>*>(smem);
-    char* data = smem + (sizeof(WideShared<V>) + 15) / 16 * 16;
+    char* data = smem + (sizeof(WideShared<V>) + 127) / 128 * 128;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const Joins m = sm.joins();
     const SeqProbe probe = probe_seqs<kWideThreads>(p);
@@ -815,17 +937,43 @@ __global__ void __launch_bounds__(kWideThreads, BMB) k_scan_bwd_wide(const __gri
     Column<XT, V> ds(data + Gates<AT, V, SHARED>::kBytes + Column<XT, V>::kBytes, warp, lane);
     const AT* ga = static_cast<const AT*>(p.a) + row0 * p.sa;
     const XT* gx = static_cast<const XT*>(p.x) + row0 * p.sx;
-    if (!SHARED && p.m_a == kRow16 && live == kAllRows) as.load16(ga + t.c0, dir * p.sa, t.nc);
-    else as.load(ga + gcol, dir * p.sa, live, 1.0f);
-    if (p.m_x == kRow16 && live == kAllRows) xs.load16(gx + t.c0, dir * p.sx, t.nc);
-    else xs.load(gx + col, dir * p.sx, live, 0.0f);
     const XT* gd = static_cast<const XT*>(p.dh) + row0 * p.sdh;
-    if (p.m_dh == kRow16 && p.dh && live == kAllRows) ds.load16(gd + t.c0, dir * p.sdh, t.nc);
-    else ds.load(gd + col, dir * p.sdh, p.dh ? live : 0u, 0.0f);
+    const bool full = live == kAllRows;
+    const bool tile_a = !SHARED && full && p.m_a == kTma, tile_x = full && p.m_x == kTma;
+    const bool tile_d = full && p.dh && p.m_dh == kTma;
+    unsigned long long* bar = &sm.bar[warp];
+    if (lane == 0) {
+        barrier_init(bar);
+        barrier_expect(bar, tile_a * as.kRunBytes + (tile_x + tile_d) * xs.kRunBytes);
+        if (tile_x) tile_load(xs.run, &maps.x, t.c0, (int)row0, bar);
+        if (tile_a) tile_load(as.run, &maps.a, t.c0, (int)row0, bar);
+        if (tile_d) tile_load(ds.run, &maps.d, t.c0, (int)row0, bar);
+    }
+    __syncwarp();
+    if constexpr (SHARED) {
+        if (t.c0 / p.group == (t.c0 + t.nc - 1) / p.group) as.load_rows(ga + t.c0 / p.group, dir * p.sa, live);
+        else as.load_lanes(ga + col / p.group, dir * p.sa, live);
+    } else if (!tile_a) {
+        if (full && p.m_a == kRow16) as.load16(ga + t.c0, dir * p.sa, t.nc);
+        else as.load(ga + gcol, dir * p.sa, live, 1.0f);
+    }
+    if (!tile_x) {
+        if (full && p.m_x == kRow16) xs.load16(gx + t.c0, dir * p.sx, t.nc);
+        else xs.load(gx + col, dir * p.sx, live, 0.0f);
+    }
+    if (!tile_d) {
+        if (full && p.dh && p.m_dh == kRow16) ds.load16(gd + t.c0, dir * p.sdh, t.nc);
+        else ds.load(gd + col, dir * p.sdh, p.dh ? live : 0u, 0.0f);
+    }
     __syncthreads();
     mark_rows<kWideRun, kWideThreads>(p, sm.marks(), t, probe, p.dh_last, p.dh0);
     cp_async_wait();
+    if (!barrier_wait(bar) && !barrier_wait(bar)) sm.flags[0] = 1;
     __syncthreads();
+    if (sm.flags[0]) {  // cannot happen while the copies' addresses are valid
+        if (tid == 0 && p.hdr) raise_status(p.hdr, GS_ERR_TIMEOUT);
+        return;
+    }
     const unsigned starts = sm.start[warp], finishes = p.dh_last ? sm.finish[warp] : 0u;
     const bool plain = (starts | finishes) == 0 && live == kAllRows;
 
@@ -969,7 +1117,7 @@ __global__ void __launch_bounds__(kWideThreads, BMB) k_scan_bwd_wide(const __gri
     };
     const bool shared = SHARED || p.group > 1;
     float* part_sum = p.part;
-    if (p.partial) part_sum += ((long long)t.cb * p.rows + row0) * p.part_gates + gcol - t.c0 / p.group;
+    if (p.partial) part_sum += ((long long)(t.c0 / p.bc) * p.rows + row0) * p.part_gates + gcol - t.c0 / p.group;
     if (!shared) {
         if constexpr (!SHARED) {
 #pragma unroll
@@ -1147,7 +1295,7 @@ __host__ __device__ inline size_t narrow_mem(const ScanParams& p, int xs, int as
     char* wa = take((size_t)kNarrowWarps * p.bc * 4);
     char* wb = take((size_t)kNarrowWarps * p.bc * 4);
     char* ca = take((size_t)p.bc * 4);
-    char* fl = take(16);
+    char* fl = take(32);
     char* wf = take(kNarrowWarps * 4);
     if (m) {
         m->x = x;
@@ -1517,21 +1665,21 @@ template <typename AT> int launch_tail(const ScanParams& p, bool bwd, cudaStream
 }
 
 template <typename XT, typename AT, int V, bool SHARED>
-int launch_wide_fwd(const ScanParams& p, bool coupled, cudaStream_t s) {
+int launch_wide_fwd(const ScanParams& p, const ScanMaps& maps, bool coupled, cudaStream_t s) {
     auto k = coupled ? k_scan_fwd_wide<XT, AT, V, SHARED, true> : k_scan_fwd_wide<XT, AT, V, SHARED, false>;
     const int smem = wide_smem<XT, AT, V, SHARED>(false);
     opt_in_smem(k, smem);
-    k<<<(unsigned)p.n_chunks * (unsigned)p.n_blocks, kWideThreads, smem, s>>>(p); note_launch();
+    k<<<(unsigned)p.n_chunks * (unsigned)p.n_chains, kWideThreads, smem, s>>>(p, maps); note_launch();
     GS_LAUNCH_CHECK();
     return GS_OK;
 }
 
 template <typename XT, typename AT, int V, bool SHARED>
-int launch_wide_bwd(const ScanParams& p, bool coupled, cudaStream_t s) {
+int launch_wide_bwd(const ScanParams& p, const ScanMaps& maps, bool coupled, cudaStream_t s) {
     auto k = coupled ? k_scan_bwd_wide<XT, AT, V, SHARED, true> : k_scan_bwd_wide<XT, AT, V, SHARED, false>;
     const int smem = wide_smem<XT, AT, V, SHARED>(true);
     opt_in_smem(k, smem);
-    k<<<(unsigned)p.n_chunks * (unsigned)p.n_blocks, kWideThreads, smem, s>>>(p); note_launch();
+    k<<<(unsigned)p.n_chunks * (unsigned)p.n_chains, kWideThreads, smem, s>>>(p, maps); note_launch();
     return launch_tail<AT>(p, true, s);
 }
 
@@ -1541,24 +1689,24 @@ int launch_narrow(const ScanParams& p, bool coupled, bool bwd, cudaStream_t s) {
     auto k = bwd ? (coupled ? k_scan_bwd_narrow<XT, AT, V, true> : k_scan_bwd_narrow<XT, AT, V, false>)
                  : (coupled ? k_scan_fwd_narrow<XT, AT, V, true> : k_scan_fwd_narrow<XT, AT, V, false>);
     opt_in_smem(k, 227 * 1024);
-    k<<<(unsigned)p.n_chunks * (unsigned)p.n_blocks, kNarrowThreads, smem, s>>>(p); note_launch();
+    k<<<(unsigned)p.n_chunks * (unsigned)p.n_chains, kNarrowThreads, smem, s>>>(p); note_launch();
     return launch_tail<AT>(p, bwd, s);
 }
 
 template <typename XT, typename AT>
-int launch_half_type(const ScanParams& p, bool wide, int v, bool coupled, bool bwd, cudaStream_t s) {
+int launch_half_type(const ScanParams& p, const ScanMaps& maps, bool wide, int v, bool coupled, bool bwd, cudaStream_t s) {
     if (!wide) return launch_narrow<XT, AT, 1>(p, coupled, bwd, s);
     const bool shared = p.group > 1;
     if (bwd) {
-        if (v == 1) return launch_wide_bwd<XT, AT, 1, false>(p, coupled, s);
-        return shared ? launch_wide_bwd<XT, AT, 2, true>(p, coupled, s)
-                      : launch_wide_bwd<XT, AT, 2, false>(p, coupled, s);
+        if (v == 1) return launch_wide_bwd<XT, AT, 1, false>(p, maps, coupled, s);
+        return shared ? launch_wide_bwd<XT, AT, 2, true>(p, maps, coupled, s)
+                      : launch_wide_bwd<XT, AT, 2, false>(p, maps, coupled, s);
     }
-    if (v == 1) return launch_wide_fwd<XT, AT, 1, false>(p, coupled, s);
+    if (v == 1) return launch_wide_fwd<XT, AT, 1, false>(p, maps, coupled, s);
     if (v == 2)
-        return shared ? launch_wide_fwd<XT, AT, 2, true>(p, coupled, s)
-                      : launch_wide_fwd<XT, AT, 2, false>(p, coupled, s);
-    return shared ? launch_wide_fwd<XT, AT, 4, true>(p, coupled, s) : launch_wide_fwd<XT, AT, 4, false>(p, coupled, s);
+        return shared ? launch_wide_fwd<XT, AT, 2, true>(p, maps, coupled, s)
+                      : launch_wide_fwd<XT, AT, 2, false>(p, maps, coupled, s);
+    return shared ? launch_wide_fwd<XT, AT, 4, true>(p, maps, coupled, s) : launch_wide_fwd<XT, AT, 4, false>(p, maps, coupled, s);
 }
 
 }  // namespace
