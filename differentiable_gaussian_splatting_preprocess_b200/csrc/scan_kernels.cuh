@@ -49,7 +49,10 @@ struct ScanRecord {  // 16 bytes, published with one 128-bit store
     unsigned tag;    // 2 * (epoch + 1) + (1 when B is the state itself)
     unsigned pad;
 };
-constexpr int kGroup = 8;  // chunks of a group
+#ifndef KGRP
+#define KGRP 8
+#endif
+constexpr int kGroup = KGRP;  // chunks of a group
 
 struct ScanParams {
     long long rows, seq_len;
@@ -530,11 +533,28 @@ __device__ __forceinline__ bool join_chunks(const ScanParams& p, const Tile& t, 
         unsigned spin = 0;
         // the state after group g - 1, from that of the nearest group that has one
         auto state = [&]() {
-            for (int u = r.group; u >= 0 && ok; --u) {
-                const ScanRecord* q = grec + tid - (ptrdiff_t)(u + 1) * stride;
-                ScanRecord v = poll(q);
-                while (ok && !(v.tag == t.tag + 1u || (u < r.group && v.tag == t.tag))) ok = again(p, q, v, spin);
-                S = v.tag & 1u ? v.B : apply(v.A, v.B, S);
+            if (r.group == 0) {
+                const ScanRecord* q = grec + tid - (ptrdiff_t)stride;
+                ScanRecord w = poll(q);
+                while (ok && w.tag != t.tag + 1u) ok = again(p, q, w, spin);
+                S = w.B;
+                return;
+            }
+            constexpr int kBatch = 4;  // records in one round trip
+#pragma unroll 1
+            for (int top = r.group; top >= 0; top -= kBatch) {
+                ScanRecord w[kBatch];
+#pragma unroll
+                for (int i = 0; i < kBatch; ++i)
+                    if (top >= i) w[i] = poll(grec + tid - (ptrdiff_t)(top - i + 1) * stride);
+#pragma unroll
+                for (int i = 0; i < kBatch; ++i) {
+                    if (top < i) continue;
+                    // the farthest one has to have its state, the others at least their composites
+                    while (ok && !(w[i].tag == t.tag + 1u || (top - i < r.group && w[i].tag == t.tag)))
+                        ok = again(p, grec + tid - (ptrdiff_t)(top - i + 1) * stride, w[i], spin);
+                    S = w[i].tag & 1u ? w[i].B : apply(w[i].A, w[i].B, S);
+                }
             }
         };
         if (mine && ok) {
