@@ -58,10 +58,9 @@ k_scan_step(long long n, int C, int G, int group, int coupled, long long sa, lon
 int elem_size(int dtype) { return dtype == GS_F32 ? 4 : 2; }
 
 constexpr int kMostLanes = 4;
-#ifndef MV
-#define MV 4
-#endif
-int most_lanes(int dtype, bool bwd) { return (dtype == GS_F32 ? MV / 2 : MV) / (bwd && MV == 4 ? 2 : 1); }
+// Forward: 8 bytes of inputs to a lane; backward half of that, for its
+// registers.
+int most_lanes(int dtype, bool bwd) { return (dtype == GS_F32 ? 2 : 4) / (bwd ? 2 : 1); }
 
 struct Plan {
     ScanParams p;

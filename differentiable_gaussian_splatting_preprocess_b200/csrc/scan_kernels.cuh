@@ -10,6 +10,7 @@
 #pragma once
 
 #include <climits>
+#include <type_traits>
 
 #include <cuda.h>  // CUtensorMap
 #include <cuda_bf16.h>
@@ -25,16 +26,7 @@ constexpr int kWideThreads = 128, kNarrowThreads = 256;
 // Wide: long runs, since a warp's work per run beside its rows (finding the
 // tile, its marks, the joins) costs as much as a dozen rows.  Narrow: odd, so
 // that the runs of a warp start in different banks.
-#ifndef WRUN
-#define WRUN 32
-#endif
-#ifndef FMB
-#define FMB 3
-#endif
-#ifndef BMB
-#define BMB 4
-#endif
-constexpr int kWideRun = WRUN;
+constexpr int kWideRun = 32;
 constexpr int narrow_run(int v) { return v >= 3 ? 11 : 17; }
 constexpr unsigned kSpinLimit = 1u << 20;
 
@@ -49,10 +41,7 @@ struct ScanRecord {  // 16 bytes, published with one 128-bit store
     unsigned tag;    // 2 * (epoch + 1) + (1 when B is the state itself)
     unsigned pad;
 };
-#ifndef KGRP
-#define KGRP 8
-#endif
-constexpr int kGroup = KGRP;  // chunks of a group
+constexpr int kGroup = 8;  // chunks of a group
 
 struct ScanParams {
     long long rows, seq_len;
@@ -777,7 +766,7 @@ __device__ __forceinline__ void wide_carry(const WideShared<V>& sm, int warp, in
 }
 
 template <typename XT, typename AT, int V, bool SHARED, bool COUPLED>
-__global__ void __launch_bounds__(kWideThreads, FMB) k_scan_fwd_wide(const __grid_constant__ ScanParams p,
+__global__ void __launch_bounds__(kWideThreads, 3) k_scan_fwd_wide(const __grid_constant__ ScanParams p,
                                                                    const __grid_constant__ ScanMaps maps) {
     extern __shared__ __align__(128) char smem[];
     WideShared<V>& sm = *reinterpret_cast<WideShared<V>*>(smem);
@@ -932,7 +921,7 @@ __device__ __forceinline__ void sum_rows(float (&s)[8], int bits, int lane) {
 }
 
 template <typename XT, typename AT, int V, bool SHARED, bool COUPLED>
-__global__ void __launch_bounds__(kWideThreads, BMB) k_scan_bwd_wide(const __grid_constant__ ScanParams p,
+__global__ void __launch_bounds__(kWideThreads, 4) k_scan_bwd_wide(const __grid_constant__ ScanParams p,
                                                                    const __grid_constant__ ScanMaps maps) {
     extern __shared__ __align__(128) char smem[];
     WideShared<V>& sm = *reinterpret_cast<WideShared<V>*>(smem);
@@ -1003,13 +992,14 @@ __global__ void __launch_bounds__(kWideThreads, BMB) k_scan_bwd_wide(const __gri
         for (int v = 0; v < V; ++v)
             f[v] = p.h0 ? p.h0[(size_t)sm.start_seq[pr_of(r)] * p.C + col + v] : 0.0f;
     };
+    auto last = [&](int r, float (&f)[V]) {
+#pragma unroll
+        for (int v = 0; v < V; ++v) f[v] += p.dh_last[(size_t)sm.finish_seq[pr_of(r)] * p.C + col + v];
+    };
     // gradient a row's state receives from outside the recurrence
     auto upstream = [&](int r, float (&f)[V]) {
         ds.get(r, f);
-        if ((finishes >> r) & 1u) {
-#pragma unroll
-            for (int v = 0; v < V; ++v) f[v] += p.dh_last[(size_t)sm.finish_seq[pr_of(r)] * p.C + col + v];
-        }
+        if ((finishes >> r) & 1u) last(r, f);
     };
     // The run's action on the state (A, B) and on the adjoint (A, K), and the
     // former at the run's parts of kPart rows: the states in front of a part's
@@ -1085,134 +1075,136 @@ __global__ void __launch_bounds__(kWideThreads, BMB) k_scan_bwd_wide(const __gri
     XT* pdx = static_cast<XT*>(p.dx) + end * p.sdx + col;
     AT* pda = static_cast<AT*>(p.da) + end * p.sda + gcol;
     const unsigned store = active ? live : 0u;
-    // What a gate's gradient multiplies: the state before the row (coupled:
-    // less x), for the rows of one part.
-    float hp[kPart][V];
-    auto states_of = [&](int part) {
-        float hs[V];
-        const bool cut = starts & ((1u << (part * kPart)) - 1u);
+    const bool shared = SHARED || p.group > 1;
+    // gates shared by lanes: the whole warp, an aligned group of a power of two, or any run of lanes
+    const int gl = p.group / V;
+    const bool whole = t.c0 / p.group == (t.c0 + t.nc - 1) / p.group;
+    const bool even = whole || (gl < 32 && (gl & (gl - 1)) == 0 && gl * V == p.group);
+    const int bits = whole ? 5 : 31 - __clz(gl), nb = min(bits, 3);
+    const bool writes = (whole || active) && (lane & ((1 << bits) - 1)) < kPart;  // idle lanes hold sums too
+    unsigned same = 0;
+    if (shared && active && !even) {
 #pragma unroll
-        for (int v = 0; v < V; ++v) hs[v] = cut ? Bp[part][v] : apply(Ap[part][v], Bp[part][v], h[v]);
+        for (int i = 0; i < 5; ++i) {
+            const int o = lane + (1 << i);
+            if (o < 32 && o * V < t.nc && (t.c0 + o * V) / p.group == gcol) same |= 1u << i;
+        }
+    }
+    const bool head = active && (lane == 0 || (col - V) / p.group != gcol);
+    AT* pda0 = static_cast<AT*>(p.da) + row0 * p.sda + gcol;
+    float* part0 = p.part;
+    if (p.partial) part0 += ((long long)(t.c0 / p.bc) * p.rows + row0) * p.part_gates + gcol - t.c0 / p.group;
+    auto write = [&](int r, float v) {
+        if (!((live >> r) & 1u)) return;
+        if (p.partial) part0[r * spart] = v;
+        else pda0[r * sda] = from_f<AT>(v);
+    };
+    // One part: the states in front of its rows, then the adjoint backwards
+    // through them.  MARKED: some row of the run starts or finishes a sequence
+    // or belongs to none.  (One copy of this code for all parts: unrolled over
+    // the run it ran out of the instruction cache.)
+    auto do_part = [&](int part, auto marked) {
+        constexpr bool MARKED = decltype(marked)::value;
+        const int first_row = part * kPart;
+        const unsigned st = starts >> first_row, lv = store >> first_row;
+        Column<XT, V> px = xs, pd = ds;
+        Gates<AT, V, SHARED> pa = as;
+        px.s += first_row * px.kRow, pd.s += first_row * pd.kRow;
+        pa.s += first_row * pa.kRow;
+        if constexpr (SHARED) pa.at += first_row * pa.pitch;
+        float hs[V], hp[kPart][V];  // hp: what a gate's gradient multiplies, the state before the row (coupled: less x)
+        const bool cut = starts & ((1u << first_row) - 1u);
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            float a = Ap[0][v], b = Bp[0][v];
+#pragma unroll
+            for (int i = 1; i < kParts; ++i) {
+                a = part == i ? Ap[i][v] : a;
+                b = part == i ? Bp[i][v] : b;
+            }
+            hs[v] = cut ? b : apply(a, b, h[v]);
+        }
 #pragma unroll
         for (int i = 0; i < kPart; ++i) {
-            const int r = part * kPart + i;
-            if (r >= kWideRun) continue;
-            step_fence(r);
+            step_fence(i);
             float av[V], uv[V];
-            as.wide(r, av);
-            xs.get(r, uv);
-            if (!plain && ((starts >> r) & 1u)) first(r, hs);
+            pa.wide(i, av);
+            px.get(i, uv);
+            if (MARKED && ((st >> i) & 1u)) first(first_row + i, hs);
 #pragma unroll
             for (int v = 0; v < V; ++v) hp[i][v] = COUPLED ? hs[v] - uv[v] : hs[v];
             if (COUPLED) rest_v<V>(uv, av, uv);
             fma_v<V>(hs, av, hs, uv);
         }
-    };
-    // the adjoint of row r: writes dx, returns the products of the gate's gradient
-    auto reverse_row = [&](int r, float (&dav)[V]) {
-        float av[V], g[V], dxv[V];
-        as.wide(r, av);
-        if (plain) ds.get(r, g);
-        else upstream(r, g);
-        add_v<V>(g, g, K);
-        mul_v<V>(dav, g, hp[r % kPart]);
-        if (COUPLED) {
-            rest_v<V>(dxv, av, g);
-        } else {
+        float s[kPart];
 #pragma unroll
-            for (int v = 0; v < V; ++v) dxv[v] = g[v];
-        }
-        mul_v<V>(K, av, g);
-        if (!plain && ((starts >> r) & 1u)) {
-            if (p.dh0 && active) {
-                float* d = p.dh0 + (size_t)sm.start_seq[pr_of(r)] * p.C + col;
-#pragma unroll
-                for (int v = 0; v < V; ++v) d[v] = K[v];
-            }
-#pragma unroll
-            for (int v = 0; v < V; ++v) K[v] = 0.0f;
-        }
-        pdx -= sdx;
-        if ((store >> r) & 1u) Pack<XT, V>::store(pdx, dxv);
-    };
-    const bool shared = SHARED || p.group > 1;
-    float* part_sum = p.part;
-    if (p.partial) part_sum += ((long long)(t.c0 / p.bc) * p.rows + row0) * p.part_gates + gcol - t.c0 / p.group;
-    if (!shared) {
-        if constexpr (!SHARED) {
-#pragma unroll
-            for (int part = kParts - 1; part >= 0; --part) {
-                states_of(part);
-#pragma unroll
-                for (int i = kPart - 1; i >= 0; --i) {
-                    const int r = part * kPart + i;
-                    if (r >= kWideRun) continue;
-                    step_fence(r);
-                    float dav[V];
-                    reverse_row(r, dav);
-                    pda -= sda;
-                    if ((store >> r) & 1u) Pack<AT, V>::store(pda, dav);
-                }
-            }
-        }
-    } else {
-        pda -= kWideRun * sda;
-        auto write = [&](int r, float v) {
-            if (!((live >> r) & 1u)) return;
-            if (p.partial) part_sum[r * spart] = v;
-            else pda[r * sda] = from_f<AT>(v);
-        };
-        // lanes of one gate: the whole warp, an aligned group of a power of two, or any run of lanes
-        const int gl = p.group / V;
-        const bool whole = t.c0 / p.group == (t.c0 + t.nc - 1) / p.group;
-        const bool even = whole || (gl < 32 && (gl & (gl - 1)) == 0 && gl * V == p.group);
-        const int bits = whole ? 5 : 31 - __clz(gl), nb = min(bits, 3);
-        const bool writes = (whole || active) && (lane & ((1 << bits) - 1)) < kPart;  // idle lanes hold sums too
-        unsigned same = 0;
-        if (active && !even) {
-#pragma unroll
-            for (int i = 0; i < 5; ++i) {
-                const int o = lane + (1 << i);
-                if (o < 32 && o * V < t.nc && (t.c0 + o * V) / p.group == gcol) same |= 1u << i;
-            }
-        }
-        const bool head = active && (lane == 0 || (col - V) / p.group != gcol);
-#pragma unroll
-        for (int part = kParts - 1; part >= 0; --part) {
-            states_of(part);
-            float s[kPart];
-#pragma unroll
-            for (int i = kPart - 1; i >= 0; --i) {
-                const int r = part * kPart + i;
-                s[i] = 0.0f;
-                if (r >= kWideRun) continue;
-                step_fence(r);
-                float dav[V];
-                reverse_row(r, dav);
-                if (active) {
-#pragma unroll
-                    for (int v = 0; v < V; ++v) s[i] += dav[v];
-                }
-            }
-            if (even) {
-                sum_rows(s, bits, lane);
-#pragma unroll
-                for (int i = 0; i < kPart; ++i)
-                    if ((i << nb) < kPart && writes) write(part * kPart + (lane & ((1 << nb) - 1)) + (i << nb), s[i]);
+        for (int i = kPart - 1; i >= 0; --i) {
+            step_fence(i);
+            float av[V], g[V], dav[V], dxv[V];
+            pa.wide(i, av);
+            pd.get(i, g);
+            if (MARKED && ((finishes >> (first_row + i)) & 1u)) last(first_row + i, g);
+            add_v<V>(g, g, K);
+            mul_v<V>(dav, g, hp[i]);
+            if (COUPLED) {
+                rest_v<V>(dxv, av, g);
             } else {
 #pragma unroll
-                for (int i = 0; i < kPart; ++i) {
-                    float v = s[i];
+                for (int v = 0; v < V; ++v) dxv[v] = g[v];
+            }
+            mul_v<V>(K, av, g);
+            if (MARKED && ((st >> i) & 1u)) {
+                if (p.dh0 && active) {
+                    float* d = p.dh0 + (size_t)sm.start_seq[pr_of(first_row + i)] * p.C + col;
 #pragma unroll
-                    for (int b = 0; b < 5; ++b) {
-                        const float o = __shfl_down_sync(~0u, v, 1 << b);
-                        if ((same >> b) & 1u) v += o;
-                    }
-                    if (head) write(part * kPart + i, v);
+                    for (int v = 0; v < V; ++v) d[v] = K[v];
+                }
+#pragma unroll
+                for (int v = 0; v < V; ++v) K[v] = 0.0f;
+            }
+            pdx -= sdx;
+            const bool in = MARKED ? (lv >> i) & 1u : active;
+            if (in) Pack<XT, V>::store(pdx, dxv);
+            if (!shared) {
+                pda -= sda;
+                if constexpr (!SHARED) {
+                    if (in) Pack<AT, V>::store(pda, dav);
                 }
             }
+            s[i] = 0.0f;
+            if (active) {
+#pragma unroll
+                for (int v = 0; v < V; ++v) s[i] += dav[v];
+            }
         }
+        if (!shared) return;
+        if (even) {
+            sum_rows(s, bits, lane);
+#pragma unroll
+            for (int i = 0; i < kPart; ++i)
+                if ((i << nb) < kPart && writes) write(first_row + (lane & ((1 << nb) - 1)) + (i << nb), s[i]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < kPart; ++i) {
+                float v = s[i];
+#pragma unroll
+                for (int b = 0; b < 5; ++b) {
+                    const float o = __shfl_down_sync(~0u, v, 1 << b);
+                    if ((same >> b) & 1u) v += o;
+                }
+                if (head) write(first_row + i, v);
+            }
+        }
+    };
+    static_assert(kWideRun % kPart == 0, "whole parts");
+    if (plain) {
+#pragma unroll 1
+        for (int part = kParts - 1; part >= 0; --part) do_part(part, std::false_type{});
+    } else {
+#pragma unroll 1
+        for (int part = kParts - 1; part >= 0; --part) do_part(part, std::true_type{});
     }
+    pda = pda0;
     if (p.zero_pad && active && live != kAllRows) {
         const float z[V] = {};
         for (int r = 0; r < kWideRun; ++r, pdx += sdx, pda += sda) {
