@@ -53,6 +53,8 @@ def rasterize(means: torch.Tensor, scales: torch.Tensor, quats: torch.Tensor, op
 
 def _evenly(t: torch.Tensor) -> torch.Tensor:
     """The tensor itself where its rows are evenly spaced, else a contiguous copy."""
+    if t.is_contiguous():
+        return t
     try:
         B.row_stride(t)
     except ValueError:
@@ -68,22 +70,25 @@ def scan_workspace(a: torch.Tensor, x: torch.Tensor, seq_offsets: Optional[torch
     return torch.zeros(max(n, 16), dtype=torch.uint8, device=x.device)
 
 
+def _scan(a, x, h0, seq_offsets, reverse, coupled, final_only, workspace, with_states):
+    """(h, h_last, states, workspace) of the recurrence; rows in front of and
+    behind all sequences give zeros."""
+    pad = seq_offsets is not None
+    # the layout of a new h is that of a contiguous x, which a plan without h describes
+    plan = B.scan_plan(a, x, seq_offsets, reverse, coupled, pad)
+    if workspace is None and plan.ws_bytes:
+        workspace = torch.zeros(plan.ws_bytes, dtype=torch.uint8, device=x.device)
+    h = None if final_only else torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    h_last = torch.empty((plan.n_seq, plan.channels), dtype=torch.float32, device=x.device)
+    states = torch.empty(plan.states_bytes // 4, dtype=torch.float32, device=x.device) if with_states else None
+    B.gs_scan_fwd(a, x, h, h_last, states, workspace, h0, seq_offsets, reverse, coupled, pad)
+    return h, h_last, states, workspace
+
+
 class _GatedScan(torch.autograd.Function):
     @staticmethod
     def forward(ctx, a, x, h0, seq_offsets, reverse, coupled, final_only, workspace):
-        a, x = _evenly(a), _evenly(x)
-        h0 = None if h0 is None else h0.contiguous()
-        d = B.scan_desc(a, x, seq_offsets)
-        if workspace is None:
-            need = B.gs_scan_workspace_bytes(d)
-            workspace = torch.zeros(need, dtype=torch.uint8, device=x.device) if need else None
-        h = None if final_only else torch.empty(x.shape, dtype=x.dtype, device=x.device)
-        h_last = torch.empty((d.n_seq, d.channels), dtype=torch.float32, device=x.device)
-        states = None
-        if any(ctx.needs_input_grad[:3]):
-            states = torch.empty(B.gs_scan_states_bytes(d) // 4, dtype=torch.float32, device=x.device)
-        B.gs_scan_fwd(a, x, h, h_last, states, workspace, h0, seq_offsets, reverse, coupled,
-                      zero_pad=seq_offsets is not None)
+        h, h_last, states, workspace = _scan(a, x, h0, seq_offsets, reverse, coupled, final_only, workspace, True)
         ctx.save_for_backward(a, x, h0, seq_offsets, states)
         ctx.mode, ctx.workspace = (reverse, coupled), workspace
         ctx.set_materialize_grads(False)
@@ -99,7 +104,7 @@ class _GatedScan(torch.autograd.Function):
         dh0 = torch.empty_like(h0) if h0 is not None and ctx.needs_input_grad[2] else None
         B.gs_scan_bwd(a, x, states, da, dx, None if dh is None else _evenly(dh),
                       None if dh_last is None else dh_last.contiguous(), dh0, ctx.workspace, h0, seq_offsets, reverse,
-                      coupled, zero_pad=seq_offsets is not None)
+                      coupled, seq_offsets is not None)
         return da, dx, dh0, None, None, None, None, None
 
 
@@ -124,7 +129,11 @@ def gated_scan(a: torch.Tensor, x: torch.Tensor, h0: Optional[torch.Tensor] = No
     Differentiable (once) w.r.t. ``a``, ``x`` and ``h0``.  ``workspace``: from
     scan_workspace, kept by the caller across calls; the backward uses it
     again.  None: one is made for the call."""
-    return _GatedScan.apply(a, x, h0, seq_offsets, reverse, coupled, final_only, workspace)
+    if torch.is_grad_enabled() and (a.requires_grad or x.requires_grad or (h0 is not None and h0.requires_grad)):
+        return _GatedScan.apply(_evenly(a), _evenly(x), None if h0 is None else h0.contiguous(), seq_offsets, reverse,
+                                coupled, final_only, workspace)
+    return _scan(_evenly(a), _evenly(x), None if h0 is None else h0.contiguous(), seq_offsets, reverse, coupled,
+                 final_only, workspace, False)[:2]
 
 
 def scan_step(a: torch.Tensor, x: torch.Tensor, state: torch.Tensor, out_state: Optional[torch.Tensor] = None,
@@ -133,8 +142,8 @@ def scan_step(a: torch.Tensor, x: torch.Tensor, state: torch.Tensor, out_state: 
     C], ``state`` float32 [n, C]; returns (h of x's type, new state).  The new
     state goes to ``out_state`` (which may be ``state``), or to a new tensor.
     Not differentiable."""
-    a, x = _evenly(a.detach()), _evenly(x.detach())
+    a, x = _evenly(a), _evenly(x)
     out = torch.empty_like(state) if out_state is None else out_state
-    h = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-    B.gs_scan_step(a, x, state.detach(), out, h, coupled)
+    h = torch.empty_like(x, memory_format=torch.contiguous_format)
+    B.gs_scan_step(a, x, state, out, h, coupled)
     return h, out

@@ -192,13 +192,14 @@ def camera_struct(cam) -> GsCamera:
     return c
 
 
-def _stream(stream) -> ctypes.c_void_p:
-    s = torch.cuda.current_stream() if stream is None else stream
-    return ctypes.c_void_p(s.cuda_stream)
+def _stream(stream) -> int:
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+    return stream.cuda_stream
 
 
-def _ptr(t: Optional[torch.Tensor]) -> Optional[ctypes.c_void_p]:
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+def _ptr(t: Optional[torch.Tensor]) -> Optional[int]:
+    return None if t is None else t.data_ptr()
 
 
 def _check(t: Optional[torch.Tensor], name: str, dtype, shape=None, optional: bool = False) -> None:
@@ -206,13 +207,15 @@ def _check(t: Optional[torch.Tensor], name: str, dtype, shape=None, optional: bo
         if optional:
             return
         raise ValueError(f"{name} is required")
+    if t.is_cuda and t.dtype is dtype and t.is_contiguous() and (shape is None or t.shape == shape):
+        return
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
     if t.dtype != dtype:
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
-    if shape is not None and tuple(t.shape) != tuple(shape):
+    if tuple(t.shape) != tuple(shape):
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
 
 
@@ -545,10 +548,10 @@ class _on_device:
     launch on (``stream``, or that device's current one)."""
 
     def __init__(self, t: torch.Tensor, stream=None):
-        self.index, self.stream, self.guard = t.device.index, stream, None
+        self.index, self.stream, self.guard = t.get_device(), stream, None
 
-    def __enter__(self) -> ctypes.c_void_p:
-        if torch.cuda.current_device() != self.index:
+    def __enter__(self) -> int:
+        if torch._C._cuda_getDevice() != self.index:
             self.guard = torch.cuda.device(self.index)
             self.guard.__enter__()
         return _stream(self.stream)
@@ -559,8 +562,9 @@ class _on_device:
 
 
 def _same_device(t: torch.Tensor, others) -> None:
+    index = t.get_device()
     for o in others:
-        if o is not None and o.device != t.device:
+        if o is not None and o.get_device() != index:
             raise ValueError(f"tensors are on different devices ({t.device} and {o.device})")
 
 
@@ -634,6 +638,43 @@ def scan_desc(a, x, seq_offsets=None, reverse: bool = False, coupled: bool = Fal
     return d
 
 
+class ScanPlan:
+    """The checked description of a scan's tensors and the sizes it needs."""
+    __slots__ = ("desc", "ref", "n_seq", "channels", "ws_bytes", "states_bytes")
+
+    def __init__(self, desc: GsScanDesc):
+        self.desc, self.ref = desc, ctypes.byref(desc)
+        self.n_seq, self.channels = desc.n_seq, desc.channels
+        self.ws_bytes, self.states_bytes = gs_scan_workspace_bytes(desc), gs_scan_states_bytes(desc)
+
+
+_plans: dict = {}  # by layout alone: types, sizes and strides of the tensors, never their addresses
+
+
+def _layout(t: Optional[torch.Tensor]):
+    return None if t is None else (t.dtype, t.shape, t.stride())
+
+
+def scan_plan(a, x, seq_offsets=None, reverse: bool = False, coupled: bool = False, zero_pad: bool = False, h=None,
+              dL_da=None, dL_dx=None, dL_dh=None) -> ScanPlan:
+    """scan_desc and its sizes, kept for the next call on tensors of the same
+    layout."""
+    key = (a.dtype, a.shape, a.stride(), x.dtype, x.shape, x.stride(),
+           None if seq_offsets is None else (seq_offsets.dtype, seq_offsets.shape), reverse, coupled, zero_pad,
+           _layout(h), _layout(dL_da), _layout(dL_dx), _layout(dL_dh))
+    plan = _plans.get(key)
+    if plan is None:
+        plan = ScanPlan(scan_desc(a, x, seq_offsets, reverse, coupled, zero_pad, h, dL_da, dL_dx, dL_dh))
+        if len(_plans) >= 1024:
+            _plans.clear()
+        _plans[key] = plan
+    if not x.is_cuda:
+        raise ValueError("x must be a CUDA tensor")
+    if seq_offsets is not None and not seq_offsets.is_contiguous():
+        raise ValueError("seq_offsets must be contiguous")
+    return plan
+
+
 def gs_scan_workspace_bytes(desc: GsScanDesc) -> int:
     return int(lib().gs_scan_workspace_bytes(ctypes.byref(desc)))
 
@@ -642,13 +683,16 @@ def gs_scan_states_bytes(desc: GsScanDesc) -> int:
     return int(lib().gs_scan_states_bytes(ctypes.byref(desc)))
 
 
-def _check_scan_states(desc: GsScanDesc, states, ws, **per_seq) -> None:
+def _check_scan_states(plan: ScanPlan, states, ws, **per_seq) -> None:
     for name, t in per_seq.items():
-        _check(t, name, torch.float32, (desc.n_seq, desc.channels), optional=True)
-    _check(states, "states", torch.float32, optional=True)
-    if states is not None and 4 * states.numel() < gs_scan_states_bytes(desc):
-        raise ValueError("states holds fewer bytes than gs_scan_states_bytes(desc)")
-    _check(ws, "ws", torch.uint8, optional=True)
+        if t is not None:
+            _check(t, name, torch.float32, (plan.n_seq, plan.channels))
+    if states is not None:
+        _check(states, "states", torch.float32)
+        if 4 * states.numel() < plan.states_bytes:
+            raise ValueError("states holds fewer bytes than gs_scan_states_bytes(desc)")
+    if ws is not None:
+        _check(ws, "ws", torch.uint8)
 
 
 def gs_scan_fwd(a, x, h=None, h_last=None, states=None, ws=None, h0=None, seq_offsets=None, reverse: bool = False,
@@ -656,12 +700,12 @@ def gs_scan_fwd(a, x, h=None, h_last=None, states=None, ws=None, h0=None, seq_of
     """Gated linear recurrence; see scan_desc for ``a``, ``x`` and
     ``seq_offsets``.  Writes ``h`` (x's type and shape), ``h_last`` [n_seq, C]
     float32 and ``states`` (float32, gs_scan_states_bytes) where given."""
-    d = scan_desc(a, x, seq_offsets, reverse, coupled, zero_pad, h=h)
-    _check_scan_states(d, states, ws, h0=h0, h_last=h_last)
+    plan = scan_plan(a, x, seq_offsets, reverse, coupled, zero_pad, h)
+    _check_scan_states(plan, states, ws, h0=h0, h_last=h_last)
     _same_device(x, (a, h, h_last, states, ws, h0, seq_offsets))
     with _on_device(x, stream) as s:
         _ok("gs_scan_fwd", lib().gs_scan_fwd(
-            ctypes.byref(d), _ptr(a), _ptr(x), _ptr(h0), _ptr(seq_offsets), _ptr(h), _ptr(h_last), _ptr(states),
+            plan.ref, a.data_ptr(), x.data_ptr(), _ptr(h0), _ptr(seq_offsets), _ptr(h), _ptr(h_last), _ptr(states),
             _ptr(ws), 0 if ws is None else ws.numel(), s))
 
 
@@ -671,31 +715,44 @@ def gs_scan_bwd(a, x, states, dL_da, dL_dx, dL_dh=None, dL_dh_last=None, dL_dh0=
     """Gradients of gs_scan_fwd's inputs (written): ``dL_da``, ``dL_dx`` and,
     where given, ``dL_dh0``, from ``dL_dh`` and ``dL_dh_last`` (None: zero) and
     the forward's ``states``."""
-    d = scan_desc(a, x, seq_offsets, reverse, coupled, zero_pad, dL_da=dL_da, dL_dx=dL_dx, dL_dh=dL_dh)
     if states is None:
         raise ValueError("states is required")
-    _check_scan_states(d, states, ws, h0=h0, dL_dh_last=dL_dh_last, dL_dh0=dL_dh0)
+    plan = scan_plan(a, x, seq_offsets, reverse, coupled, zero_pad, None, dL_da, dL_dx, dL_dh)
+    _check_scan_states(plan, states, ws, h0=h0, dL_dh_last=dL_dh_last, dL_dh0=dL_dh0)
     _same_device(x, (a, dL_da, dL_dx, dL_dh, dL_dh_last, dL_dh0, states, ws, h0, seq_offsets))
     with _on_device(x, stream) as s:
         _ok("gs_scan_bwd", lib().gs_scan_bwd(
-            ctypes.byref(d), _ptr(a), _ptr(x), _ptr(h0), _ptr(seq_offsets), _ptr(states), _ptr(dL_dh),
-            _ptr(dL_dh_last), _ptr(dL_da), _ptr(dL_dx), _ptr(dL_dh0), _ptr(ws), 0 if ws is None else ws.numel(), s))
+            plan.ref, a.data_ptr(), x.data_ptr(), _ptr(h0), _ptr(seq_offsets), states.data_ptr(), _ptr(dL_dh),
+            _ptr(dL_dh_last), dL_da.data_ptr(), dL_dx.data_ptr(), _ptr(dL_dh0), _ptr(ws),
+            0 if ws is None else ws.numel(), s))
+
+
+_step_plans: dict = {}
 
 
 def gs_scan_step(a, x, state, state_out, h=None, coupled: bool = False, stream=None) -> None:
     """One row of the recurrence per kept state: ``a`` [n, G], ``x`` [n, C],
     ``state`` and ``state_out`` [n, C] float32 (may be the same tensor),
     ``h`` [n, C] of x's type or None."""
-    if x.dim() != 2:
-        raise ValueError("x must have shape [n, C]")
-    d = scan_desc(a, x, coupled=coupled, h=h)
-    d.n_seq = d.rows
-    _check(state, "state", torch.float32, tuple(x.shape))
-    _check(state_out, "state_out", torch.float32, tuple(x.shape))
+    key = (a.dtype, a.shape, a.stride(), x.dtype, x.shape, x.stride(), coupled, _layout(h))
+    plan = _step_plans.get(key)
+    if plan is None:
+        if x.dim() != 2:
+            raise ValueError("x must have shape [n, C]")
+        d = scan_desc(a, x, coupled=coupled, h=h)
+        d.n_seq = d.rows
+        plan = (d, ctypes.byref(d))
+        if len(_step_plans) >= 1024:
+            _step_plans.clear()
+        _step_plans[key] = plan
+    if not x.is_cuda:
+        raise ValueError("x must be a CUDA tensor")
+    _check(state, "state", torch.float32, x.shape)
+    _check(state_out, "state_out", torch.float32, x.shape)
     _same_device(x, (a, state, state_out, h))
     with _on_device(x, stream) as s:
-        _ok("gs_scan_step", lib().gs_scan_step(ctypes.byref(d), _ptr(a), _ptr(x), _ptr(state), _ptr(state_out),
-                                               _ptr(h), s))
+        _ok("gs_scan_step", lib().gs_scan_step(plan[1], a.data_ptr(), x.data_ptr(), state.data_ptr(),
+                                               state_out.data_ptr(), _ptr(h), s))
 
 
 def tensor_list(tensors) -> tuple:

@@ -635,10 +635,7 @@ template <int V> struct WideShared {
 
 // Rows whose loads from shared memory are in flight together; left to itself
 // the compiler raises all rows' loads to the top and spills.
-#ifndef KSTEP
-#define KSTEP 4
-#endif
-constexpr int kStep = KSTEP;
+constexpr int kStep = 4;
 __device__ __forceinline__ void step_fence(int r) {
     if (r % kStep == 0) asm volatile("" ::: "memory");
 }

@@ -61,11 +61,14 @@ def grad_norm(grads: GradList, kind: str = "l2", out: Optional[torch.Tensor] = N
     sqrt(sum g^2) ("l2") or max |g| ("inf")."""
     if kind not in _KINDS:
         raise ValueError(f"kind must be one of {sorted(_KINDS)}, got {kind!r}")
-    if out is None:
-        with torch.cuda.stream(stream):  # None: the current stream
-            out = torch.empty(1, dtype=torch.float32, device=grads.device)
-    norm = out
-    B._same_device(grads.ws, (norm,))
+    if out is not None:
+        norm = out
+        B._same_device(grads.ws, (norm,))
+    elif stream is None:
+        norm = torch.empty(1, dtype=torch.float32, device=grads.device)
+    else:
+        with torch.cuda.stream(stream):
+            norm = torch.empty(1, dtype=torch.float32, device=grads.device)
     B.gs_grad_norm(grads.c, norm, grads.ws, _KINDS[kind], stream)
     return norm
 
