@@ -31,69 +31,143 @@ struct AdamRates {
     float max_norm, clip_eps;
 };
 
+// Which product of the two moment updates is rounded before the other one is
+// fused with the sum is fixed here, not left to the compiler, so that a
+// parameter's bits do not depend on how the elements are dealt out: the old
+// moment's for gradients taken as they are, the gradient's for gradients
+// chained through an activation (CHAINED).
+template <bool CHAINED>
 __device__ __forceinline__ float adam_update(float p, float g, float& m, float& v, float rate, const AdamRates& r) {
-    m = r.b1 * m + (1.0f - r.b1) * g;
-    v = r.b2 * v + (1.0f - r.b2) * g * g;
+    const float c1 = 1.0f - r.b1, c2 = __fmul_rn(1.0f - r.b2, g);
+    if (CHAINED) {
+        m = __fmaf_rn(r.b1, m, __fmul_rn(c1, g));
+        v = __fmaf_rn(r.b2, v, __fmul_rn(c2, g));
+    } else {
+        m = __fmaf_rn(c1, g, __fmul_rn(r.b1, m));
+        v = __fmaf_rn(c2, g, __fmul_rn(r.b2, v));
+    }
     const float m_hat = m * r.inv_bc1, v_hat = v * r.inv_bc2;
     return p - rate * m_hat / (sqrtf(v_hat) + r.eps);
 }
 
-// Work items, in order: 3N position elements, 3N log-scale elements, N
-// logit-opacity elements, C*N colour elements (element-wise), then N
-// quaternion rows (renormalised together).  Moment layout (m and v alike):
-// [means 3N | log scales 3N | quats 4N | opacity N | colours C N].
-__global__ void __launch_bounds__(kAdamBlock)
-k_adam(int N, int C, AdamRates r, float* __restrict__ means, float* __restrict__ log_scales,
-       float4* __restrict__ quats, float* __restrict__ logit_opacity, float* __restrict__ colors,
-       const float* __restrict__ g_means, const float* __restrict__ g_scales, const float4* __restrict__ g_quats,
-       const float* __restrict__ g_opacity, const float* __restrict__ g_colors, float* __restrict__ m,
-       float* __restrict__ v, float* __restrict__ scales_out, float* __restrict__ opacity_out) {
-    const size_t n = (size_t)N;
-    const size_t e_means = 3 * n, e_scales = 6 * n, e_op = 7 * n, e_col = 7 * n + (size_t)C * n, e_all = e_col + n;
-    const size_t o_scales = 3 * n, o_quats = 6 * n, o_op = 10 * n, o_col = 11 * n;
-    const size_t stride = (size_t)gridDim.x * blockDim.x;
+// One group of elements (all but the quaternions): four neighbouring elements
+// to a work item, moved by 16-byte accesses where every array of the group
+// allows it (VEC), else one by one.
+struct AdamGroup {
+    float* p;
+    const float* g;
+    float *m, *v, *out;  // out: the new activated values, or NULL
+    size_t n;            // elements
+    float rate;
+    int vec;
+};
+
+struct AdamArgs {
+    AdamGroup group[4];  // means, log scales, logit opacity, colours
+    size_t items[4];     // work items up to and with the group
+    float4* quats;
+    const float4* g_quats;
+    float *m_quats, *v_quats;
+    size_t n_quats;
+    int vec_quats;
+};
+
+enum AdamKind { kPlain = 0, kScale = 1, kOpacity = 2 };
+
+template <int KIND>
+__device__ __forceinline__ void adam_element(float& p, float g, float& m, float& v, float& out, float rate, float coef,
+                                             const AdamRates& r) {
+    if (KIND == kPlain) {
+        p = adam_update<false>(p, coef * g, m, v, rate, r);
+    } else if (KIND == kScale) {
+        const float gr = coef * g * expf(p);  // d exp(x) / dx
+        p = adam_update<true>(p, gr, m, v, rate, r);
+        out = expf(p);
+    } else {
+        const float o = 1.0f / (1.0f + expf(-p));
+        const float gr = coef * g * o * (1.0f - o);  // d sigmoid(x) / dx
+        p = adam_update<true>(p, gr, m, v, rate, r);
+        out = 1.0f / (1.0f + expf(-p));
+    }
+}
+
+template <int KIND>
+__device__ __forceinline__ void adam_item(const AdamGroup& a, size_t item, float coef, const AdamRates& r) {
+    const size_t e = 4 * item;
+    if (a.vec && e + 4 <= a.n) {
+        float4 p = *reinterpret_cast<const float4*>(a.p + e), m = *reinterpret_cast<const float4*>(a.m + e);
+        float4 v = *reinterpret_cast<const float4*>(a.v + e), o;
+        const float4 g = *reinterpret_cast<const float4*>(a.g + e);
+        adam_element<KIND>(p.x, g.x, m.x, v.x, o.x, a.rate, coef, r);
+        adam_element<KIND>(p.y, g.y, m.y, v.y, o.y, a.rate, coef, r);
+        adam_element<KIND>(p.z, g.z, m.z, v.z, o.z, a.rate, coef, r);
+        adam_element<KIND>(p.w, g.w, m.w, v.w, o.w, a.rate, coef, r);
+        *reinterpret_cast<float4*>(a.p + e) = p;
+        *reinterpret_cast<float4*>(a.m + e) = m;
+        *reinterpret_cast<float4*>(a.v + e) = v;
+        if (KIND != kPlain && a.out) *reinterpret_cast<float4*>(a.out + e) = o;
+        return;
+    }
+    const size_t end = e + 4 < a.n ? e + 4 : a.n;
+    for (size_t i = e; i < end; ++i) {
+        float p = a.p[i], m = a.m[i], v = a.v[i], o;
+        adam_element<KIND>(p, a.g[i], m, v, o, a.rate, coef, r);
+        a.p[i] = p;
+        a.m[i] = m;
+        a.v[i] = v;
+        if (KIND != kPlain && a.out) a.out[i] = o;
+    }
+}
+
+// Work items in order: the four element-wise groups, then the quaternion rows
+// (renormalised together).  Moment layout (m and v alike): [means 3N | log
+// scales 3N | quats 4N | opacity N | colours C N].
+__global__ void __launch_bounds__(kAdamBlock) k_adam(const __grid_constant__ AdamArgs a, AdamRates r) {
+    const size_t stride = (size_t)gridDim.x * blockDim.x, all = a.items[3] + a.n_quats;
     float coef = 1.0f;
     if (r.grad_norm) {
         const float q = r.max_norm / (*r.grad_norm + r.clip_eps);
         coef = q > 1.0f ? 1.0f : q;  // a NaN stays
     }
-    for (size_t i = (size_t)blockIdx.x * blockDim.x + threadIdx.x; i < e_all; i += stride) {
-        if (i < e_means) {
-            means[i] = adam_update(means[i], coef * g_means[i], m[i], v[i], r.rate[0], r);
-        } else if (i < e_scales) {
-            const size_t k = i - e_means;
-            const float ls = log_scales[k];
-            const float g = coef * g_scales[k] * expf(ls);  // d exp(x) / dx
-            const float nls = adam_update(ls, g, m[o_scales + k], v[o_scales + k], r.rate[1], r);
-            log_scales[k] = nls;
-            if (scales_out) scales_out[k] = expf(nls);
-        } else if (i < e_op) {
-            const size_t k = i - e_scales;
-            const float x = logit_opacity[k];
-            const float o = 1.0f / (1.0f + expf(-x));
-            const float g = coef * g_opacity[k] * o * (1.0f - o);  // d sigmoid(x) / dx
-            const float nx = adam_update(x, g, m[o_op + k], v[o_op + k], r.rate[3], r);
-            logit_opacity[k] = nx;
-            if (opacity_out) opacity_out[k] = 1.0f / (1.0f + expf(-nx));
-        } else if (i < e_col) {
-            const size_t k = i - e_op;
-            colors[k] = adam_update(colors[k], coef * g_colors[k], m[o_col + k], v[o_col + k], r.rate[4], r);
+    for (size_t i = (size_t)blockIdx.x * blockDim.x + threadIdx.x; i < all; i += stride) {
+        if (i < a.items[0]) {
+            adam_item<kPlain>(a.group[0], i, coef, r);
+        } else if (i < a.items[1]) {
+            adam_item<kScale>(a.group[1], i - a.items[0], coef, r);
+        } else if (i < a.items[2]) {
+            adam_item<kOpacity>(a.group[2], i - a.items[1], coef, r);
+        } else if (i < a.items[3]) {
+            adam_item<kPlain>(a.group[3], i - a.items[2], coef, r);
         } else {
-            const size_t k = i - e_col;
-            float4 q = quats[k];
-            const float4 g = g_quats[k];
-            float* mq = m + o_quats + 4 * k;
-            float* vq = v + o_quats + 4 * k;
-            q.x = adam_update(q.x, coef * g.x, mq[0], vq[0], r.rate[2], r);
-            q.y = adam_update(q.y, coef * g.y, mq[1], vq[1], r.rate[2], r);
-            q.z = adam_update(q.z, coef * g.z, mq[2], vq[2], r.rate[2], r);
-            q.w = adam_update(q.w, coef * g.w, mq[3], vq[3], r.rate[2], r);
-            const float nn = q.x * q.x + q.y * q.y + q.z * q.z + q.w * q.w;
+            const size_t k = i - a.items[3];
+            float4 q = a.quats[k], m, v;
+            const float4 g = a.g_quats[k];
+            float *mq = a.m_quats + 4 * k, *vq = a.v_quats + 4 * k;
+            if (a.vec_quats) {
+                m = *reinterpret_cast<const float4*>(mq);
+                v = *reinterpret_cast<const float4*>(vq);
+            } else {
+                m = make_float4(mq[0], mq[1], mq[2], mq[3]);
+                v = make_float4(vq[0], vq[1], vq[2], vq[3]);
+            }
+            q.x = adam_update<false>(q.x, coef * g.x, m.x, v.x, r.rate[2], r);
+            q.y = adam_update<false>(q.y, coef * g.y, m.y, v.y, r.rate[2], r);
+            q.z = adam_update<false>(q.z, coef * g.z, m.z, v.z, r.rate[2], r);
+            q.w = adam_update<false>(q.w, coef * g.w, m.w, v.w, r.rate[2], r);
+            if (a.vec_quats) {
+                *reinterpret_cast<float4*>(mq) = m;
+                *reinterpret_cast<float4*>(vq) = v;
+            } else {
+                mq[0] = m.x, mq[1] = m.y, mq[2] = m.z, mq[3] = m.w;
+                vq[0] = v.x, vq[1] = v.y, vq[2] = v.z, vq[3] = v.w;
+            }
+            const float nn = __fmaf_rn(q.w, q.w, __fmaf_rn(q.z, q.z, __fmaf_rn(q.x, q.x, __fmul_rn(q.y, q.y))));
+
             if (nn > 0.0f) {
                 const float inv = rsqrtf(nn);
                 q = make_float4(q.x * inv, q.y * inv, q.z * inv, q.w * inv);
             }
-            quats[k] = q;
+            a.quats[k] = q;
         }
     }
 }
@@ -124,12 +198,28 @@ int adam_launch(const gs_adam_config* cfg, int step, int N, int C, float* means,
     r.grad_norm = grad_norm;
     r.max_norm = max_norm;
     r.clip_eps = clip_eps;
-    const size_t items = (size_t)N * (8 + (size_t)C);
-    size_t blocks = (items + kAdamBlock - 1) / kAdamBlock;
+    const size_t n = (size_t)N;
+    AdamArgs a;
+    a.group[0] = {means, dL_dmeans, m, v, nullptr, 3 * n, r.rate[0], 0};
+    a.group[1] = {log_scales, dL_dscales, m + 3 * n, v + 3 * n, scales, 3 * n, r.rate[1], 0};
+    a.group[2] = {logit_opacity, dL_dopacity, m + 10 * n, v + 10 * n, opacity, n, r.rate[3], 0};
+    a.group[3] = {colors, dL_dcolors, m + 11 * n, v + 11 * n, nullptr, (size_t)C * n, r.rate[4], 0};
+    size_t items = 0;
+    for (int k = 0; k < 4; ++k) {
+        AdamGroup& g = a.group[k];
+        g.vec = aligned(g.p, 16) && aligned(g.g, 16) && aligned(g.m, 16) && aligned(g.v, 16) && aligned(g.out, 16);
+        items += (g.n + 3) / 4;
+        a.items[k] = items;
+    }
+    a.quats = reinterpret_cast<float4*>(quats);
+    a.g_quats = reinterpret_cast<const float4*>(dL_dquats);
+    a.m_quats = m + 6 * n;
+    a.v_quats = v + 6 * n;
+    a.n_quats = n;
+    a.vec_quats = aligned(a.m_quats, 16) && aligned(a.v_quats, 16);
+    size_t blocks = (items + n + kAdamBlock - 1) / kAdamBlock;
     if (blocks > 148u * 16u) blocks = 148u * 16u;
-    k_adam<<<(unsigned)blocks, kAdamBlock, 0, (cudaStream_t)stream>>>(
-        N, C, r, means, log_scales, reinterpret_cast<float4*>(quats), logit_opacity, colors, dL_dmeans, dL_dscales,
-        reinterpret_cast<const float4*>(dL_dquats), dL_dopacity, dL_dcolors, m, v, scales, opacity); note_launch();
+    k_adam<<<(unsigned)blocks, kAdamBlock, 0, (cudaStream_t)stream>>>(a, r); note_launch();
     GS_LAUNCH_CHECK();
     return GS_OK;
 }

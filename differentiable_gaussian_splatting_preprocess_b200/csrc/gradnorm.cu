@@ -82,9 +82,15 @@ template <typename T> struct Vec16 {
     }
 };
 
+// KEEP: left in L2 for a second reading, else marked to leave it first.
+template <bool KEEP> __device__ __forceinline__ uint4 load16(const uint4* p) {
+    if constexpr (KEEP) return __ldg(p);
+    else return __ldcs(p);
+}
+
 // One chunk [b, e) of a tensor: a head up to the first 16-byte boundary and
 // a tail element by element, 16-byte pieces between them.
-template <typename T, typename One, typename Many>
+template <bool KEEP, typename T, typename One, typename Many>
 __device__ __forceinline__ void walk(const T* g, long long b, long long e, One one, Many many) {
     constexpr int n = 16 / sizeof(T);
     long long vb = b + (long long)((16 - ((uintptr_t)(g + b) & 15)) & 15) / (long long)sizeof(T);
@@ -97,12 +103,12 @@ __device__ __forceinline__ void walk(const T* g, long long b, long long e, One o
         uint4 w[kUnroll];
 #pragma unroll
         for (int u = 0; u < kUnroll; ++u)
-            w[u] = __ldcs(reinterpret_cast<const uint4*>(g + vb) + i + u * kNormBlock);
+            w[u] = load16<KEEP>(reinterpret_cast<const uint4*>(g + vb) + i + u * kNormBlock);
 #pragma unroll
         for (int u = 0; u < kUnroll; ++u) many(vb + (long long)(i + u * kNormBlock) * n, w[u]);
     }
     for (; i < vecs; i += kNormBlock)
-        many(vb + (long long)i * n, __ldcs(reinterpret_cast<const uint4*>(g + vb) + i));
+        many(vb + (long long)i * n, load16<KEEP>(reinterpret_cast<const uint4*>(g + vb) + i));
     for (long long j = vb + (long long)vecs * n + threadIdx.x; j < e; j += kNormBlock) one(j);
 }
 
@@ -119,7 +125,7 @@ template <int N> __device__ __forceinline__ int find(const Entries<N>& l, unsign
 
 template <typename T, bool INF>
 __device__ __forceinline__ void norm_chunk(const T* g, long long b, long long e, double& sum, unsigned& top) {
-    walk(
+    walk<true>(
         g, b, e,
         [&](long long i) {
             const float f[1] = {(float)g[i]};
@@ -194,14 +200,14 @@ k_grad_norm(const __grid_constant__ Entries<N> l, NormScratch* ws, int part0, in
 template <typename T>
 __device__ __forceinline__ void clip_chunk(const T* g, T* o, long long b, long long e, float coef) {
     if ((((uintptr_t)g ^ (uintptr_t)o) & 15) == 0) {
-        walk(
+        walk<false>(
             g, b, e, [&](long long i) { o[i] = (T)((float)g[i] * coef); },
             [&](long long i, uint4 w) {
                 float f[Vec16<T>::n];
                 Vec16<T>::unpack(w, f);
 #pragma unroll
                 for (int k = 0; k < Vec16<T>::n; ++k) f[k] *= coef;
-                *reinterpret_cast<uint4*>(o + i) = Vec16<T>::pack(f);
+                __stcs(reinterpret_cast<uint4*>(o + i), Vec16<T>::pack(f));
             });
     } else {
         for (long long i = b + threadIdx.x; i < e; i += kNormBlock) o[i] = (T)((float)g[i] * coef);
@@ -213,7 +219,9 @@ __global__ void __launch_bounds__(kNormBlock)
 k_grad_clip(const __grid_constant__ Entries<N> l, const float* norm, float max_norm, float eps) {
     const float q = max_norm / (*norm + eps);
     const float coef = q > 1.0f ? 1.0f : q;  // a NaN stays
-    for (unsigned c = blockIdx.x; c < l.chunks; c += gridDim.x) {
+    // last chunks first: what the norm read last is still in L2
+    for (unsigned i = blockIdx.x; i < l.chunks; i += gridDim.x) {
+        const unsigned c = l.chunks - 1 - i;
         const Entry& t = l.e[find(l, c)];
         if (coef == 1.0f && t.src == t.dst) continue;
         const long long b = (long long)(c - t.first) * kChunk;

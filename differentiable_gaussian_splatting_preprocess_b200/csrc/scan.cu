@@ -129,7 +129,7 @@ bool make_plan(const gs_scan_desc* d, Plan* out, int most, bool packed) {
     p.partial = p.n_blocks > 1 && p.group > 1 && p.bc % p.group != 0;
     p.part_gates = p.partial ? (p.bc - 1) / p.group + 2 : 0;
     const size_t records = (size_t)p.n_chunks + (p.n_chunks + kGroup - 1) / kGroup;
-    q.rec_bytes = p.n_chunks > 1 ? records * p.n_chains * p.bc * sizeof(ScanRecord) : 0;
+    q.rec_bytes = p.n_chunks > 1 ? records * p.n_chains * p.bc * sizeof(ulonglong2) : 0;
     q.part_bytes = p.partial ? align_up((size_t)p.n_blocks * p.rows * p.part_gates * 4, 16) : 0;
     return true;
 }
@@ -203,7 +203,7 @@ int lanes_ok(const void* ptr, long long stride, int es, int most) {
 void set_workspace(Plan& q, void* ws) {
     q.p.hdr = static_cast<WsHeader*>(ws);
     char* b = static_cast<char*>(ws) + sizeof(WsHeader);
-    q.p.rec = reinterpret_cast<ScanRecord*>(b);
+    q.p.rec = reinterpret_cast<ulonglong2*>(b);
     q.p.group_rec = q.p.rec + (size_t)q.p.n_chunks * q.p.n_chains * q.p.bc;
     q.p.part = reinterpret_cast<float*>(b + q.rec_bytes);
 }

@@ -36,10 +36,12 @@ constexpr unsigned kSpinLimit = 1u << 20;
 // of each row; else element by element.
 enum CopyMode { kFlat = 0, kTma = 1, kRow16 = 2, kElem = 3 };
 
-struct ScanRecord {  // 16 bytes, published with one 128-bit store
+// Written and read as two 64-bit words, each with its own tag: a reader that
+// meets a record as it is being written sees two tags that differ (128-bit
+// accesses were seen to tear).
+struct ScanRecord {
     float A, B;
-    unsigned tag;    // 2 * (epoch + 1) + (1 when B is the state itself)
-    unsigned pad;
+    unsigned tag;  // 2 * (epoch + 1) + (1 when B is the state itself); 0: not one record
 };
 constexpr int kGroup = 8;  // chunks of a group
 
@@ -61,7 +63,7 @@ struct ScanParams {
     void *h, *da, *dx;
     float *h_last, *states, *dh0, *part;
     WsHeader* hdr;
-    ScanRecord *rec, *group_rec;  // per chunk, and per kGroup chunks
+    ulonglong2 *rec, *group_rec;  // per chunk, and per kGroup chunks
 };
 
 // TMA descriptions of a, x and dL/dh as matrices of rows x channels with boxes
@@ -232,25 +234,20 @@ template <int V> __device__ __forceinline__ void rest_v(float (&d)[V], const flo
 // that is not finite is in B already).
 __device__ __forceinline__ float apply(float A, float B, float h) { return h == 0.0f ? B : fmaf(A, h, B); }
 
-__device__ __forceinline__ void publish(ScanRecord* p, float A, float B, unsigned tag) {
-    const unsigned long long lo = (unsigned long long)__float_as_uint(B) << 32 | __float_as_uint(A);
-    const unsigned long long hi = tag;
-    asm volatile("{ .reg .b128 q; mov.b128 q, {%1, %2}; st.relaxed.gpu.global.b128 [%0], q; }" ::"l"(p), "l"(lo),
-                 "l"(hi)
+__device__ __forceinline__ void publish(ulonglong2* p, float A, float B, unsigned tag) {
+    const unsigned long long t = (unsigned long long)tag << 32;
+    asm volatile("st.relaxed.gpu.global.v2.b64 [%0], {%1, %2};" ::"l"(p), "l"(t | __float_as_uint(A)),
+                 "l"(t | __float_as_uint(B))
                  : "memory");
 }
 
-__device__ __forceinline__ ScanRecord poll(const ScanRecord* p) {
-    unsigned long long lo, hi;
-    asm volatile("{ .reg .b128 q; ld.relaxed.gpu.global.b128 q, [%2]; mov.b128 {%0, %1}, q; }"
-                 : "=l"(lo), "=l"(hi)
-                 : "l"(p)
-                 : "memory");
+__device__ __forceinline__ ScanRecord poll(const ulonglong2* p) {
+    unsigned long long a, b;
+    asm volatile("ld.relaxed.gpu.global.v2.b64 {%0, %1}, [%2];" : "=l"(a), "=l"(b) : "l"(p) : "memory");
     ScanRecord r;
-    r.A = __uint_as_float((unsigned)lo);
-    r.B = __uint_as_float((unsigned)(lo >> 32));
-    r.tag = (unsigned)hi;
-    r.pad = 0;
+    r.A = __uint_as_float((unsigned)a);
+    r.B = __uint_as_float((unsigned)b);
+    r.tag = a >> 32 == b >> 32 ? (unsigned)(a >> 32) : 0u;
     return r;
 }
 
@@ -408,7 +405,7 @@ struct Joins {
 };
 
 // Reads a record again.  False when the wait ran out.
-__device__ __forceinline__ bool again(const ScanParams& p, const ScanRecord* q, ScanRecord& r, unsigned& spin) {
+__device__ __forceinline__ bool again(const ScanParams& p, const ulonglong2* q, ScanRecord& r, unsigned& spin) {
     if (++spin > kSpinLimit || ((spin & 1023u) == 0 && *reinterpret_cast<volatile unsigned*>(&p.hdr->status))) {
         raise_status(p.hdr, GS_ERR_TIMEOUT);
         return false;
@@ -431,12 +428,12 @@ struct Ahead {
 // 2048 bf16 forward 189 us against 131 us without any joins.)
 constexpr int kLookGroups = 24;
 
-__device__ __forceinline__ bool look_ahead(const ScanParams& p, const Tile& t, const ScanRecord* rec,
-                                           const ScanRecord* grec, size_t stride, bool groups, Ahead& r) {
+__device__ __forceinline__ bool look_ahead(const ScanParams& p, const Tile& t, const ulonglong2* rec,
+                                           const ulonglong2* grec, size_t stride, bool groups, Ahead& r) {
     const int lane = threadIdx.x & 31, g = t.k / kGroup, before = t.k % kGroup;
     const bool is_chunk = lane < kGroup - 1, is_group = lane >= 8;
     const bool mine = is_chunk ? lane < before : (is_group && lane - 8 < g);
-    const ScanRecord* q = is_chunk ? rec - (ptrdiff_t)(lane + 1) * stride : grec - (ptrdiff_t)(lane - 7) * stride;
+    const ulonglong2* q = is_chunk ? rec - (ptrdiff_t)(lane + 1) * stride : grec - (ptrdiff_t)(lane - 7) * stride;
     unsigned spin = 0, tag = 0;
     while (true) {
         if (mine && (tag | 1u) != t.tag + 1u) tag = poll(q).tag;
@@ -485,7 +482,7 @@ __device__ __forceinline__ bool join_chunks(const ScanParams& p, const Tile& t, 
     }
     const size_t stride = (size_t)p.n_chains * bc, at = (size_t)t.chain * bc;
     const int g = t.k / kGroup;
-    ScanRecord *rec = p.rec + (size_t)t.k * stride + at, *grec = p.group_rec + (size_t)g * stride + at;
+    ulonglong2 *rec = p.rec + (size_t)t.k * stride + at, *grec = p.group_rec + (size_t)g * stride + at;
     const bool closes = t.k % kGroup == kGroup - 1, mine = tid < bc;
     bool known = t.k == 0;  // the state after this chunk is B, whatever comes in
 #pragma unroll
@@ -523,7 +520,7 @@ __device__ __forceinline__ bool join_chunks(const ScanParams& p, const Tile& t, 
         // the state after group g - 1, from that of the nearest group that has one
         auto state = [&]() {
             if (r.group == 0) {
-                const ScanRecord* q = grec + tid - (ptrdiff_t)stride;
+                const ulonglong2* q = grec + tid - (ptrdiff_t)stride;
                 ScanRecord w = poll(q);
                 while (ok && w.tag != t.tag + 1u) ok = again(p, q, w, spin);
                 S = w.B;

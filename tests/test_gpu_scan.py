@@ -277,6 +277,41 @@ def test_equal_inputs_give_equal_bits_and_workspaces_are_reused():
     assert B.gs_read_status(ws) == B.GS_OK
 
 
+@pytest.mark.parametrize("S,L,C,xdt", [(8, 4096, 2048, BF16), (1, 16384, 1024, F32), (4, 6000, 4, F32)])
+def test_many_chunks_in_flight(S, L, C, xdt):
+    """Hundreds of chunks wait for one another's records, in a workspace whose
+    records are those of other inputs: forward and backward against the
+    recurrence in float64, and equal bits from a fresh workspace."""
+    ws = None
+    for seed in (1, 2):
+        a, x, h0, dh, dl = _inputs(seed, S * L, C, C, S, xdt, xdt)
+        v = lambda t: t.view(S, L, C)  # noqa: E731
+        ws = GA.scan_workspace(v(a), v(x)) if ws is None else ws
+        got = _run(v(a), v(x), h0, v(dh), dl, None, workspace=ws)
+        for p, q in zip(got, _run(v(a), v(x), h0, v(dh), dl, None)):
+            assert torch.equal(p, q)
+        # the recurrence and its magnitudes, all channels and sequences at once
+        A, X, D = v(a).double(), v(x).double(), v(dh).double()
+        hs, hm = h0.double(), h0.double().abs()
+        before, before_m = torch.empty_like(A), torch.empty_like(A)
+        gam = (2 * L + 64) * U / (1 - (2 * L + 64) * U)
+        eps = torch.finfo(xdt).eps / 2
+        ok = torch.ones((), dtype=torch.bool, device="cuda")
+        for t in range(L):
+            before[:, t], before_m[:, t] = hs, hm
+            hs, hm = A[:, t] * hs + X[:, t], A[:, t] * hm + X[:, t].abs()
+            ok &= ((got[0][:, t].double() - hs).abs() <= gam * hm * (1 + eps) + eps * hs.abs()).all()
+        assert ok and ((got[1].double() - hs).abs() <= (gam + U) * hm).all()
+        k, km = dl.double(), dl.double().abs()
+        for t in range(L - 1, -1, -1):
+            g, gm = D[:, t] + k, D[:, t].abs() + km
+            ok &= ((got[3][:, t].double() - g).abs() <= gam * gm * (1 + eps) + eps * g.abs()).all()
+            w, wm = g * before[:, t], gm * before_m[:, t]
+            ok &= ((got[2][:, t].double() - w).abs() <= 2 * gam * wm * (1 + eps) + eps * w.abs()).all()
+            k, km = A[:, t] * g, A[:, t] * gm
+        assert ok and ((got[4].double() - k).abs() <= (gam + U) * km).all()
+
+
 def test_captured_forward_and_backward_replay():
     T, C = 3000, 48
     a, x, h0, dh, dl = _inputs(5, T, C, C, 1, F32, F32)
