@@ -302,6 +302,7 @@ def run_ours(args):
                                 logit_opacity=torch.logit(opacity), colors=colors.clone()))
         if sh_deg is not None:
             raise SystemExit("--adam covers RGB colours (no --sh-degree)")
+        from differentiable_gaussian_splatting_preprocess_b200 import optim
         adam["m"] = torch.zeros((11 + 3) * sc.N, device=dev)
         adam["v"] = torch.zeros_like(adam["m"])
         # the optimiser updates its own copies and writes the activated
@@ -377,8 +378,16 @@ def run_ours(args):
             timed("allreduce", lambda: MV.allreduce_grads(grads))
         if adam is not None:
             adam["step"][0] += 1
-            timed("adam", lambda: B.gs_adam_step(adam["cfg"], adam["step"][0], adam["params"], grads, adam["m"],
-                                                 adam["v"], adam["scales"], adam["opacity"]))
+            if args.max_grad_norm is None:
+                timed("adam", lambda: B.gs_adam_step(adam["cfg"], adam["step"][0], adam["params"], grads, adam["m"],
+                                                     adam["v"], adam["scales"], adam["opacity"]))
+            else:
+                if "list" not in adam:
+                    adam["list"] = optim.GradList(list(grads.values()))
+                timed("grad_norm", lambda: adam.update(norm=optim.grad_norm(adam["list"], out=adam.get("norm"))))
+                timed("adam", lambda: B.gs_adam_step_clipped(
+                    adam["cfg"], adam["step"][0], adam["params"], grads, adam["m"], adam["v"], adam["norm"],
+                    args.max_grad_norm, adam["scales"], adam["opacity"]))
 
     for _ in range(args.warmup):
         flush.zero_()
@@ -640,6 +649,8 @@ def main():
     ap.add_argument("--adam", action="store_true",
                     help="add the fused optimiser step (gs_adam_step) to the step (eager timing only: the step "
                          "number changes every step)")
+    ap.add_argument("--max-grad-norm", type=float, default=None,
+                    help="with --adam: clip the gradients to this norm (gs_grad_norm, gs_adam_step_clipped)")
     ap.add_argument("--sh-f16", action="store_true",
                     help="with --sh-degree: store the SH coefficients in binary16 (the mixed-precision variant)")
     args = ap.parse_args()

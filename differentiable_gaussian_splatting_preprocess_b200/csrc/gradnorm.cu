@@ -97,7 +97,7 @@ __device__ __forceinline__ void walk(const T* g, long long b, long long e, One o
     if (vb > e) vb = e;
     const int vecs = (int)((e - vb) / n);
     for (long long i = b + threadIdx.x; i < vb; i += kNormBlock) one(i);
-    constexpr int kUnroll = 4;
+    constexpr int kUnroll = 8;
     int i = threadIdx.x;
     for (; i + (kUnroll - 1) * kNormBlock < vecs; i += kUnroll * kNormBlock) {
         uint4 w[kUnroll];

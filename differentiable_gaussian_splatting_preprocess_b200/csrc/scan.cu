@@ -31,25 +31,39 @@ namespace {
 
 constexpr int kStepThreads = 256;
 
-// One row of the recurrence for every kept state: elementwise.
-template <typename XT, typename AT, int V>
+// One row of the recurrence for every kept state: elementwise, V neighbouring
+// channels to a thread (V = 4 where their gates and alignment allow one access
+// each).  I: 32-bit item numbers where they suffice, for the division.
+template <typename XT, typename AT, int V, typename I>
 __global__ void __launch_bounds__(kStepThreads)
-k_scan_step(long long n, int C, int G, int group, int coupled, long long sa, long long sx, long long sh, const AT* a,
-            const XT* x, const float* state, float* state_out, XT* h) {
-    const int per = C / V;
-    for (long long i = (long long)blockIdx.x * kStepThreads + threadIdx.x; i < n * per;
-         i += (long long)gridDim.x * kStepThreads) {
-        const long long r = i / per;
+k_scan_step(I items, int C, int group, int coupled, long long sa, long long sx, long long sh, const AT* a, const XT* x,
+            const float* state, float* state_out, XT* h) {
+    const I per = (I)(C / V), stride = (I)gridDim.x * kStepThreads;
+    for (I i = (I)blockIdx.x * kStepThreads + threadIdx.x; i < items; i += stride) {
+        const I r = i / per;
         const int c = (int)(i - r * per) * V;
+        float av[V], u[V], s[V];
+        Pack<XT, V> px;
+        px.load(x + (long long)r * sx + c);
+        const AT* ga = a + (long long)r * sa;
+        if (group == 1) {
+            Pack<AT, V> pa;
+            pa.load(ga + c);
+            pa.get(av);
+        } else {
+            const float g = to_f<AT>(ga[c / group]);
 #pragma unroll
-        for (int v = 0; v < V; ++v) {
-            const float av = to_f<AT>(a[r * sa + (group == 1 ? c + v : (c + v) / group)]);
-            float u = to_f<XT>(x[r * sx + c + v]);
-            if (coupled) u *= 1.0f - av;
-            const float s = fmaf(av, state[r * C + c + v], u);
-            state_out[r * C + c + v] = s;
-            if (h) h[r * sh + c + v] = from_f<XT>(s);
+            for (int v = 0; v < V; ++v) av[v] = g;
         }
+        Pack<float, V> ps;
+        ps.load(state + (long long)r * C + c);
+        px.get(u);
+        ps.get(s);
+        if (coupled) rest_v<V>(u, av, u);
+        fma_v<V>(s, av, s, u);
+        Pack<float, V>::store(state_out + (long long)r * C + c, s);
+        if (h) Pack<XT, V>::store(h + (long long)r * sh + c, s);
+        if (stride > items - i) break;  // (no wrap of the item number)
     }
 }
 
@@ -223,18 +237,35 @@ bool set_sequences(Plan& q, const long long* offsets) {
     return true;
 }
 
+template <typename XT, typename AT, int V>
+int launch_step_v(const gs_scan_desc* d, const void* a, const void* x, const float* state, float* state_out, void* h,
+                  cudaStream_t s) {
+    const long long items = d->rows * (d->channels / V);
+    long long blocks = (items + kStepThreads - 1) / kStepThreads;
+    if (blocks > 148 * 16) blocks = 148 * 16;
+    const int group = d->channels / d->gates, coupled = (d->flags & GS_SCAN_COUPLED) != 0;
+    if (items < 0x7fffffffll)
+        k_scan_step<XT, AT, V, unsigned><<<(unsigned)blocks, kStepThreads, 0, s>>>(
+            (unsigned)items, d->channels, group, coupled, d->stride_a, d->stride_x, d->stride_h,
+            static_cast<const AT*>(a), static_cast<const XT*>(x), state, state_out, static_cast<XT*>(h));
+    else
+        k_scan_step<XT, AT, V, unsigned long long><<<(unsigned)blocks, kStepThreads, 0, s>>>(
+            (unsigned long long)items, d->channels, group, coupled, d->stride_a, d->stride_x, d->stride_h,
+            static_cast<const AT*>(a), static_cast<const XT*>(x), state, state_out, static_cast<XT*>(h));
+    note_launch();
+    GS_LAUNCH_CHECK();
+    return GS_OK;
+}
+
 template <typename XT, typename AT>
 int launch_step(const gs_scan_desc* d, const void* a, const void* x, const float* state, float* state_out, void* h,
                 cudaStream_t s) {
-    const long long n = d->rows * d->channels;
-    long long blocks = (n + kStepThreads - 1) / kStepThreads;
-    if (blocks > 148 * 8) blocks = 148 * 8;
-    k_scan_step<XT, AT, 1><<<(unsigned)blocks, kStepThreads, 0, s>>>(
-        d->rows, d->channels, d->gates, d->channels / d->gates, (d->flags & GS_SCAN_COUPLED) != 0, d->stride_a,
-        d->stride_x, d->stride_h, static_cast<const AT*>(a), static_cast<const XT*>(x), state, state_out,
-        static_cast<XT*>(h)); note_launch();
-    GS_LAUNCH_CHECK();
-    return GS_OK;
+    const int group = d->channels / d->gates;
+    bool four = d->channels % 4 == 0 && (group == 1 || group % 4 == 0) && aligned(state, 16) && aligned(state_out, 16);
+    four = four && lanes_ok(x, d->stride_x, sizeof(XT), 4) == 4 && (!h || lanes_ok(h, d->stride_h, sizeof(XT), 4) == 4);
+    four = four && (group > 1 || lanes_ok(a, d->stride_a, sizeof(AT), 4) == 4);
+    return four ? launch_step_v<XT, AT, 4>(d, a, x, state, state_out, h, s)
+                : launch_step_v<XT, AT, 1>(d, a, x, state, state_out, h, s);
 }
 
 }  // namespace

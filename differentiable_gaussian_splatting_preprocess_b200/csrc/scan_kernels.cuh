@@ -614,6 +614,14 @@ __device__ __forceinline__ Tile begin_tile(const ScanParams& p, bool descending,
     return t;
 }
 
+// A ticket past the last tile: the workspace was not zero-filled (or a call
+// before this one did not end).  Nothing is touched.
+__device__ __forceinline__ bool tile_ok(const ScanParams& p, const Tile& t) {
+    if ((unsigned)t.k < (unsigned)p.n_chunks) return true;
+    if (threadIdx.x == 0) raise_status(p.hdr, GS_ERR_INDEX);
+    return false;
+}
+
 // ---- wide tiles -----------------------------------------------------------
 
 constexpr int kWideWarps = kWideThreads / 32;
@@ -769,6 +777,7 @@ __global__ void __launch_bounds__(kWideThreads, 3) k_scan_fwd_wide(const __grid_
     const Joins m = sm.joins();
     const SeqProbe probe = probe_seqs<kWideThreads>(p);
     const Tile t = begin_tile(p, p.reverse, sm.flags);
+    if (!tile_ok(p, t)) return;
     if (tid < kWideWarps) sm.start[tid] = sm.finish[tid] = 0;
     if (tid == 0) sm.flags[0] = 0;
 
@@ -924,6 +933,7 @@ __global__ void __launch_bounds__(kWideThreads, 4) k_scan_bwd_wide(const __grid_
     const Joins m = sm.joins();
     const SeqProbe probe = probe_seqs<kWideThreads>(p);
     const Tile t = begin_tile(p, !p.reverse, sm.flags);
+    if (!tile_ok(p, t)) return;
     if (tid < kWideWarps) sm.start[tid] = sm.finish[tid] = 0;
     if (tid == 0) sm.flags[0] = 0;
 
@@ -1355,7 +1365,7 @@ __device__ __forceinline__ void join_runs(const ScanParams& p, const Joins& m, b
 template <typename XT, typename AT, int V, bool COUPLED>
 __global__ void __launch_bounds__(kNarrowThreads, V == 1 ? 4 : 3) k_scan_fwd_narrow(const __grid_constant__ ScanParams p) {
     constexpr int RUN = narrow_run(V);
-    extern __shared__ __align__(16) char smem[];
+    extern __shared__ __align__(128) char smem[];
     NarrowMem m;
     narrow_mem(p, sizeof(XT), sizeof(AT), false, smem, &m);
     const int tid = threadIdx.x, warp = tid >> 5;
@@ -1363,6 +1373,7 @@ __global__ void __launch_bounds__(kNarrowThreads, V == 1 ? 4 : 3) k_scan_fwd_nar
     const int run = tid >> p.lpr_log2, lane = tid & ((1 << p.lpr_log2) - 1);
     const SeqProbe probe = probe_seqs<kNarrowThreads>(p);
     const Tile t = begin_tile(p, p.reverse, m.j.flags);
+    if (!tile_ok(p, t)) return;
     XT* sx = reinterpret_cast<XT*>(m.x);
     AT* sa = reinterpret_cast<AT*>(m.a);
     load_tile(sx, static_cast<const XT*>(p.x), p.sx, t, p.bt, p.C, p.m_x, 0.0f);
@@ -1443,7 +1454,7 @@ __global__ void __launch_bounds__(kNarrowThreads, V == 1 ? 4 : 3) k_scan_fwd_nar
 template <typename XT, typename AT, int V, bool COUPLED>
 __global__ void __launch_bounds__(kNarrowThreads, V == 1 ? 4 : 3) k_scan_bwd_narrow(const __grid_constant__ ScanParams p) {
     constexpr int RUN = narrow_run(V);
-    extern __shared__ __align__(16) char smem[];
+    extern __shared__ __align__(128) char smem[];
     NarrowMem m;
     narrow_mem(p, sizeof(XT), sizeof(AT), true, smem, &m);
     const int tid = threadIdx.x, warp = tid >> 5;
@@ -1451,6 +1462,7 @@ __global__ void __launch_bounds__(kNarrowThreads, V == 1 ? 4 : 3) k_scan_bwd_nar
     const int run = tid >> p.lpr_log2, lane = tid & (lpr - 1);
     const SeqProbe probe = probe_seqs<kNarrowThreads>(p);
     const Tile t = begin_tile(p, !p.reverse, m.j.flags);
+    if (!tile_ok(p, t)) return;
     XT* sx = reinterpret_cast<XT*>(m.x);
     AT* sa = reinterpret_cast<AT*>(m.a);
     XT* sg = reinterpret_cast<XT*>(m.g);

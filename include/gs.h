@@ -64,7 +64,7 @@ extern "C" {
 #define GS_ERR_CUDA 8          /* a CUDA launch or copy failed */
 #define GS_ERR_UNIMPLEMENTED 16
 #define GS_ERR_OVERFLOW 32     /* device: pair count does not fit in 32 bits */
-#define GS_ERR_INDEX 64        /* device, debug build only: an index check failed (the access was skipped) */
+#define GS_ERR_INDEX 64        /* device: an index check failed and the access was skipped (debug build; gs_scan_*: the workspace was not zero-filled) */
 
 /* Stages for gs_workspace_bytes(). */
 #define GS_STAGE_PREPROCESS_FWD 0
@@ -451,7 +451,9 @@ GS_API size_t gs_scan_states_bytes(const gs_scan_desc* desc);
  *   backward follows): the state in front of every chunk of rows.
  * ws: >= gs_scan_workspace_bytes(desc) bytes, 16-byte aligned (may be NULL
  *   when that is 0).  A wait between chunks that runs out raises
- *   GS_ERR_TIMEOUT in its status word; the outputs are then incomplete.
+ *   GS_ERR_TIMEOUT in its status word, a workspace that was not zero-filled
+ *   GS_ERR_INDEX; the outputs are then incomplete, and the workspace has to
+ *   be zero-filled before it is used again.
  */
 GS_API int gs_scan_fwd(const gs_scan_desc* desc, const void* a, const void* x, const float* h0,
                        const long long* seq_offsets, void* h, float* h_last, float* states, void* ws,

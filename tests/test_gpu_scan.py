@@ -374,6 +374,26 @@ def test_bad_offsets_stay_inside_the_tensors():
         assert B.gs_read_status(ws) == B.GS_OK
 
 
+def test_a_wait_that_runs_out_and_a_workspace_that_was_not_zeroed():
+    """With the first ticket already taken nobody works on the first tile: the
+    tiles behind it wait, give up within the wait's limit and say so, and the
+    ticket past the end touches nothing."""
+    T, C = 4000, 64
+    a, x, h0, _, _ = _inputs(5, T, C, C, 1, F32, F32)
+    ws = GA.scan_workspace(a, x)
+    ws.view(torch.int64)[1] = 1
+    h, last = torch.full_like(x, 3.0), torch.empty_like(h0)
+    B.gs_scan_fwd(a, x, h, last, None, ws, h0)
+    assert B.gs_read_status(ws) & (B.GS_ERR_TIMEOUT | B.GS_ERR_INDEX) == B.GS_ERR_TIMEOUT | B.GS_ERR_INDEX
+    assert (h[:128] == 3.0).all()
+    ws.zero_()
+    B.gs_scan_fwd(a, x, h, last, None, ws, h0)
+    assert B.gs_read_status(ws) == B.GS_OK
+    with torch.no_grad():
+        want, wlast = GA.gated_scan(a, x, h0)
+    assert torch.equal(h, want) and torch.equal(last, wlast)
+
+
 def test_no_rows():
     h0 = torch.randn(3, 4, device="cuda")
     off = torch.zeros(4, dtype=torch.int64, device="cuda")
