@@ -141,7 +141,7 @@ bool make_plan(const gs_scan_desc* d, Plan* out, int most, bool packed) {
     p.n_chunks = (int)chunks;
     p.n_chains = (int)chains;
     p.partial = p.n_blocks > 1 && p.group > 1 && p.bc % p.group != 0;
-    p.part_gates = p.partial ? (p.bc - 1) / p.group + 2 : 0;
+    p.part_gates = !p.partial ? 0 : (p.group % p.bc == 0 ? 1 : (p.bc - 1) / p.group + 2);
     const size_t records = (size_t)p.n_chunks + (p.n_chunks + kGroup - 1) / kGroup;
     q.rec_bytes = p.n_chunks > 1 ? records * p.n_chains * p.bc * sizeof(ulonglong2) : 0;
     q.part_bytes = p.partial ? align_up((size_t)p.n_blocks * p.rows * p.part_gates * 4, 16) : 0;
@@ -223,10 +223,11 @@ void set_workspace(Plan& q, void* ws) {
 }
 
 int launch_typed(const Plan& q, const ScanMaps& maps, const gs_scan_desc* d, bool bwd, cudaStream_t s) {
-    const bool c = (d->flags & GS_SCAN_COUPLED) != 0, g32 = d->gate_dtype == GS_F32;
-    if (d->dtype == GS_F32) return scan_launch_f32(q.p, maps, q.wide, q.v, c, bwd, s);
-    return d->dtype == GS_BF16 ? scan_launch_bf16(q.p, maps, g32, q.wide, q.v, c, bwd, s)
-                               : scan_launch_f16(q.p, maps, g32, q.wide, q.v, c, bwd, s);
+    const bool coupled = (d->flags & GS_SCAN_COUPLED) != 0, g32 = d->gate_dtype == GS_F32;
+    ScanLaunch* launch = d->dtype == GS_F32    ? scan_launch_f32
+                         : d->dtype == GS_BF16 ? (g32 ? scan_launch_bf16_f32 : scan_launch_bf16)
+                                               : (g32 ? scan_launch_f16_f32 : scan_launch_f16);
+    return launch(q.p, maps, q.wide, q.v, coupled, bwd, s);
 }
 
 bool set_sequences(Plan& q, const long long* offsets) {

@@ -1,9 +1,9 @@
-// Gated linear recurrence: kernels with bfloat16 inputs, gates of either type.
+// Gated linear recurrence: kernels with bfloat16 inputs and gates.
 #include "scan_kernels.cuh"
 
 namespace gs {
-int scan_launch_bf16(const ScanParams& p, const ScanMaps& maps, bool gate_f32, bool wide, int v, bool coupled, bool bwd, cudaStream_t s) {
-    return gate_f32 ? launch_half_type<__nv_bfloat16, float>(p, maps, wide, v, coupled, bwd, s)
-                    : launch_half_type<__nv_bfloat16, __nv_bfloat16>(p, maps, wide, v, coupled, bwd, s);
+int scan_launch_bf16(const ScanParams& p, const ScanMaps& maps, bool wide, int v, bool coupled, bool bwd,
+                     cudaStream_t s) {
+    return launch_half_type<__nv_bfloat16, __nv_bfloat16>(p, maps, wide, v, coupled, bwd, s);
 }
 }  // namespace gs

@@ -72,11 +72,11 @@ struct ScanMaps {
     CUtensorMap a, x, d;
 };
 
-// Launches the scan (bwd: its adjoint) of one element type; `wide` and `v`
-// as chosen by the plan.
-int scan_launch_f32(const ScanParams& p, const ScanMaps& maps, bool wide, int v, bool coupled, bool bwd, cudaStream_t s);
-int scan_launch_bf16(const ScanParams& p, const ScanMaps& maps, bool gate_f32, bool wide, int v, bool coupled, bool bwd, cudaStream_t s);
-int scan_launch_f16(const ScanParams& p, const ScanMaps& maps, bool gate_f32, bool wide, int v, bool coupled, bool bwd, cudaStream_t s);
+// Launches the scan (bwd: its adjoint) of one type of inputs (and of gates:
+// the same, or fp32); `wide` and `v` as chosen by the plan.
+using ScanLaunch = int(const ScanParams& p, const ScanMaps& maps, bool wide, int v, bool coupled, bool bwd,
+                       cudaStream_t s);
+ScanLaunch scan_launch_f32, scan_launch_bf16, scan_launch_bf16_f32, scan_launch_f16, scan_launch_f16_f32;
 
 namespace {
 

@@ -108,7 +108,9 @@ def test_one_sequence(T, C, xdt, adt):
 @pytest.mark.parametrize("coupled", [False, True])
 @pytest.mark.parametrize("xdt", [F32, BF16])
 @pytest.mark.parametrize("T,C,G", [(700, 3, 1), (700, 6, 2), (900, 64, 1), (900, 96, 1), (500, 192, 2), (500, 144, 3),
-                                   (400, 128, 8), (333, 130, 65), (260, 1, 1), (600, 20, 4), (300, 640, 10)])
+                                   (400, 128, 8), (333, 130, 65), (260, 1, 1), (600, 20, 4), (300, 640, 10), (500, 8, 2),
+                                   (500, 12, 1), (3000, 16, 1), (500, 16, 4), (500, 9, 3), (500, 15, 5), (400, 12, 4),
+                                   (300, 256, 1), (300, 24, 2), (200, 68, 17)])
 def test_shared_gates_ragged(T, C, G, xdt, reverse, coupled):
     rng = np.random.default_rng(T + C)
     cuts = np.sort(rng.integers(0, T + 1, 13))
