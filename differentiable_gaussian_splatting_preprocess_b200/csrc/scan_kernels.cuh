@@ -1328,8 +1328,8 @@ __host__ __device__ inline size_t narrow_mem(const ScanParams& p, int xs, int as
 // Composites of the runs of one warp, and of what lies before (up) or behind
 // (down) this lane's run inside the warp; the warp's own goes to wA/wB/wf.
 template <int V>
-__device__ __forceinline__ void join_runs(const ScanParams& p, const Joins& m, bool up, int ch, int f, float (&A)[V],
-                                          float (&B)[V], int& fe, float (&Ae)[V], float (&Be)[V]) {
+__device__ __forceinline__ void join_runs(const ScanParams& p, const Joins& m, bool up, int ch, int f, float A,
+                                          float (&B)[V], int& fe, float& Ae, float (&Be)[V]) {
     const int lane32 = threadIdx.x & 31, warp = threadIdx.x >> 5, lpr = 1 << p.lpr_log2;
     auto shift = [&](auto v, int d) { return up ? __shfl_up_sync(~0u, v, d) : __shfl_down_sync(~0u, v, d); };
     auto has = [&](int d) { return up ? lane32 >= d : lane32 + d < 32; };
@@ -1337,29 +1337,29 @@ __device__ __forceinline__ void join_runs(const ScanParams& p, const Joins& m, b
     for (int d = 1; d < 32; d <<= 1) {
         if (d < lpr) continue;
         const int fo = shift(f, d);
+        const float Ao = shift(A, d);
+        const bool takes = has(d) && !f;
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-            const float Ao = shift(A[v], d), Bo = shift(B[v], d);
-            if (has(d) && !f) {
-                B[v] = apply(A[v], B[v], Bo);
-                A[v] *= Ao;
-            }
+            const float Bo = shift(B[v], d);
+            if (takes) B[v] = apply(A, B[v], Bo);
         }
+        if (takes) A *= Ao;
         if (has(d)) f |= fo;
     }
     if (up ? lane32 >= 32 - lpr : lane32 < lpr) {
 #pragma unroll
-        for (int v = 0; v < V; ++v) m.wA[warp * p.bc + ch + v] = A[v], m.wB[warp * p.bc + ch + v] = B[v];
+        for (int v = 0; v < V; ++v) m.wA[warp * p.bc + ch + v] = A, m.wB[warp * p.bc + ch + v] = B[v];
         m.wf[warp] = f;
     }
     fe = shift(f, lpr);
+    Ae = shift(A, lpr);
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-        Ae[v] = shift(A[v], lpr);
         Be[v] = shift(B[v], lpr);
-        if (!has(lpr)) Ae[v] = 1.0f, Be[v] = 0.0f;
+        if (!has(lpr)) Be[v] = 0.0f;
     }
-    if (!has(lpr)) fe = 0;
+    if (!has(lpr)) fe = 0, Ae = 1.0f;
 }
 
 template <typename XT, typename AT, int V, bool COUPLED>
@@ -1394,6 +1394,7 @@ __global__ void __launch_bounds__(kNarrowThreads, V == 1 ? 4 : 3) k_scan_fwd_nar
     XT* px = sx + pr0 * p.C + col;
     const AT* pa = sa + pr0 * p.G + col / p.group;
     const int dx = step * p.C, da = step * p.G;
+    // (the channels of a lane share their gate, so one product A serves them all)
     auto row = [&](int r, float (&av)[V], float (&uv)[V]) {
         Pack<XT, V> xv;
         xv.load(px + r * dx);
@@ -1408,16 +1409,16 @@ __global__ void __launch_bounds__(kNarrowThreads, V == 1 ? 4 : 3) k_scan_fwd_nar
         for (int v = 0; v < V; ++v)
             f[v] = p.h0 ? p.h0[(size_t)m.mk.start_seq[pr0 + step * r] * p.C + col + v] : 0.0f;
     };
-    float A[V], B[V], Ae[V], Be[V];
+    float A = 1.0f, B[V], Ae, Be[V];
 #pragma unroll
-    for (int v = 0; v < V; ++v) A[v] = 1.0f, B[v] = 0.0f;
+    for (int v = 0; v < V; ++v) B[v] = 0.0f;
 #pragma unroll 6
     for (int r = 0; r < RUN; ++r) {
         float av[V], uv[V];
         row(r, av, uv);
         if ((starts >> r) & 1u) first(r, B);
         fma_v<V>(B, av, B, uv);
-        mul_v<V>(A, A, av);
+        A *= av[0];
     }
     int fe;
     join_runs<V>(p, m.j, true, ch, starts != 0, A, B, fe, Ae, Be);
@@ -1428,7 +1429,7 @@ __global__ void __launch_bounds__(kNarrowThreads, V == 1 ? 4 : 3) k_scan_fwd_nar
 #pragma unroll
         for (int v = 0; v < V; ++v) {
             h[v] = warp_carry(p, m.j, warp, ch + v, m.j.carry[ch + v], true);
-            h[v] = fe ? Be[v] : apply(Ae[v], Be[v], h[v]);
+            h[v] = fe ? Be[v] : apply(Ae, Be[v], h[v]);
         }
         const bool keep = p.h && active;
 #pragma unroll 6
@@ -1516,9 +1517,9 @@ __global__ void __launch_bounds__(kNarrowThreads, V == 1 ? 4 : 3) k_scan_bwd_nar
             for (int v = 0; v < V; ++v) dv[v] += q[v];
         }
     };
-    float A[V], B[V], K[V], Ae[V], Be[V];
+    float A = 1.0f, B[V], K[V], Ae, Be[V];
 #pragma unroll
-    for (int v = 0; v < V; ++v) A[v] = 1.0f, B[v] = 0.0f, K[v] = 0.0f;
+    for (int v = 0; v < V; ++v) B[v] = 0.0f, K[v] = 0.0f;
 #pragma unroll 6
     for (int r = 0; r < RUN; ++r) {
         float av[V], uv[V];
@@ -1527,7 +1528,7 @@ __global__ void __launch_bounds__(kNarrowThreads, V == 1 ? 4 : 3) k_scan_bwd_nar
         if (COUPLED) rest_v<V>(uv, av, uv);
         if ((starts >> r) & 1u) first(r, B);
         fma_v<V>(B, av, B, uv);
-        mul_v<V>(A, A, av);
+        A *= av[0];
     }
 #pragma unroll 6
     for (int r = RUN - 1; r >= 0; --r) {
@@ -1542,16 +1543,14 @@ __global__ void __launch_bounds__(kNarrowThreads, V == 1 ? 4 : 3) k_scan_bwd_nar
         }
     }
     // the state in front of this run
-    float A2[V], h[V];
-#pragma unroll
-    for (int v = 0; v < V; ++v) A2[v] = A[v];
+    float h[V];
     int fe;
-    join_runs<V>(p, m.j, true, ch, starts != 0, A2, B, fe, Ae, Be);
+    join_runs<V>(p, m.j, true, ch, starts != 0, A, B, fe, Ae, Be);
     __syncthreads();
 #pragma unroll
     for (int v = 0; v < V; ++v) {
         h[v] = warp_carry(p, m.j, warp, ch + v, active ? p.states[(size_t)t.chunk * p.C + col + v] : 0.0f, true);
-        h[v] = fe ? Be[v] : apply(Ae[v], Be[v], h[v]);
+        h[v] = fe ? Be[v] : apply(Ae, Be[v], h[v]);
     }
     __syncthreads();
     join_runs<V>(p, m.j, false, ch, starts != 0, A, K, fe, Ae, Be);
@@ -1560,7 +1559,7 @@ __global__ void __launch_bounds__(kNarrowThreads, V == 1 ? 4 : 3) k_scan_bwd_nar
 #pragma unroll
         for (int v = 0; v < V; ++v) {
             K[v] = warp_carry(p, m.j, warp, ch + v, m.j.carry[ch + v], false);
-            K[v] = fe ? Be[v] : apply(Ae[v], Be[v], K[v]);
+            K[v] = fe ? Be[v] : apply(Ae, Be[v], K[v]);
         }
         // What a gate's gradient multiplies: the state before the row (coupled:
         // less x).  fp32 inputs hand it their place in shared memory.
