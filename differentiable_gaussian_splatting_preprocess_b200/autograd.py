@@ -71,26 +71,29 @@ def scan_workspace(a: torch.Tensor, x: torch.Tensor, seq_offsets: Optional[torch
 
 
 def _scan(a, x, h0, seq_offsets, reverse, coupled, final_only, workspace, with_states):
-    """(h, h_last, states, workspace) of the recurrence; rows in front of and
-    behind all sequences give zeros."""
-    pad = seq_offsets is not None
-    # the layout of a new h is that of a contiguous x, which a plan without h describes
-    plan = B.scan_plan(a, x, seq_offsets, reverse, coupled, pad)
+    """(h, h_last, states, workspace, plan) of the recurrence; rows in front
+    of and behind all sequences give zeros."""
+    # (a plan without h describes a contiguous one)
+    plan = B.scan_plan(a, x, seq_offsets, reverse, coupled, seq_offsets is not None)
     if workspace is None and plan.ws_bytes:
         workspace = torch.zeros(plan.ws_bytes, dtype=torch.uint8, device=x.device)
-    h = None if final_only else torch.empty(x.shape, dtype=x.dtype, device=x.device)
-    h_last = torch.empty((plan.n_seq, plan.channels), dtype=torch.float32, device=x.device)
-    states = torch.empty(plan.states_bytes // 4, dtype=torch.float32, device=x.device) if with_states else None
-    B.gs_scan_fwd(a, x, h, h_last, states, workspace, h0, seq_offsets, reverse, coupled, pad)
-    return h, h_last, states, workspace
+    B._check_scan_states(plan, None, workspace, h0=h0)
+    B._same_device(x, (a, workspace, h0, seq_offsets))
+    dev = x.device
+    h = None if final_only else torch.empty(x.shape, dtype=x.dtype, device=dev)
+    h_last = torch.empty((plan.n_seq, plan.channels), dtype=torch.float32, device=dev)
+    states = torch.empty(plan.states_bytes // 4, dtype=torch.float32, device=dev) if with_states else None
+    B._scan_fwd(plan, a, x, h, h_last, states, workspace, h0, seq_offsets)
+    return h, h_last, states, workspace, plan
 
 
 class _GatedScan(torch.autograd.Function):
     @staticmethod
     def forward(ctx, a, x, h0, seq_offsets, reverse, coupled, final_only, workspace):
-        h, h_last, states, workspace = _scan(a, x, h0, seq_offsets, reverse, coupled, final_only, workspace, True)
+        h, h_last, states, ctx.workspace, ctx.plan = _scan(a, x, h0, seq_offsets, reverse, coupled, final_only,
+                                                           workspace, True)
         ctx.save_for_backward(a, x, h0, seq_offsets, states)
-        ctx.mode, ctx.workspace = (reverse, coupled), workspace
+        ctx.mode = (reverse, coupled)
         ctx.set_materialize_grads(False)
         return h, h_last
 
@@ -98,13 +101,17 @@ class _GatedScan(torch.autograd.Function):
     @torch.autograd.function.once_differentiable
     def backward(ctx, dh, dh_last):
         a, x, h0, seq_offsets, states = ctx.saved_tensors
-        reverse, coupled = ctx.mode
         da = torch.empty(a.shape, dtype=a.dtype, device=a.device)
         dx = torch.empty(x.shape, dtype=x.dtype, device=x.device)
         dh0 = torch.empty_like(h0) if h0 is not None and ctx.needs_input_grad[2] else None
-        B.gs_scan_bwd(a, x, states, da, dx, None if dh is None else _evenly(dh),
-                      None if dh_last is None else dh_last.contiguous(), dh0, ctx.workspace, h0, seq_offsets, reverse,
-                      coupled, seq_offsets is not None)
+        if dh_last is not None:
+            dh_last = dh_last.contiguous()
+        if dh is None or dh.is_contiguous():
+            B._scan_bwd(ctx.plan, a, x, states, da, dx, dh, dh_last, dh0, ctx.workspace, h0, seq_offsets)
+        else:
+            reverse, coupled = ctx.mode
+            B.gs_scan_bwd(a, x, states, da, dx, _evenly(dh), dh_last, dh0, ctx.workspace, h0, seq_offsets, reverse,
+                          coupled, seq_offsets is not None)
         return da, dx, dh0, None, None, None, None, None
 
 

@@ -703,6 +703,11 @@ def gs_scan_fwd(a, x, h=None, h_last=None, states=None, ws=None, h0=None, seq_of
     plan = scan_plan(a, x, seq_offsets, reverse, coupled, zero_pad, h)
     _check_scan_states(plan, states, ws, h0=h0, h_last=h_last)
     _same_device(x, (a, h, h_last, states, ws, h0, seq_offsets))
+    _scan_fwd(plan, a, x, h, h_last, states, ws, h0, seq_offsets, stream)
+
+
+def _scan_fwd(plan, a, x, h, h_last, states, ws, h0, seq_offsets, stream=None) -> None:
+    """The call alone, on tensors that have been checked."""
     with _on_device(x, stream) as s:
         _ok("gs_scan_fwd", lib().gs_scan_fwd(
             plan.ref, a.data_ptr(), x.data_ptr(), _ptr(h0), _ptr(seq_offsets), _ptr(h), _ptr(h_last), _ptr(states),
@@ -720,6 +725,12 @@ def gs_scan_bwd(a, x, states, dL_da, dL_dx, dL_dh=None, dL_dh_last=None, dL_dh0=
     plan = scan_plan(a, x, seq_offsets, reverse, coupled, zero_pad, None, dL_da, dL_dx, dL_dh)
     _check_scan_states(plan, states, ws, h0=h0, dL_dh_last=dL_dh_last, dL_dh0=dL_dh0)
     _same_device(x, (a, dL_da, dL_dx, dL_dh, dL_dh_last, dL_dh0, states, ws, h0, seq_offsets))
+    _scan_bwd(plan, a, x, states, dL_da, dL_dx, dL_dh, dL_dh_last, dL_dh0, ws, h0, seq_offsets, stream)
+
+
+def _scan_bwd(plan, a, x, states, dL_da, dL_dx, dL_dh, dL_dh_last, dL_dh0, ws, h0, seq_offsets, stream=None) -> None:
+    """The call alone, on tensors that have been checked.  A forward's plan
+    serves where dL_da, dL_dx and dL_dh are contiguous."""
     with _on_device(x, stream) as s:
         _ok("gs_scan_bwd", lib().gs_scan_bwd(
             plan.ref, a.data_ptr(), x.data_ptr(), _ptr(h0), _ptr(seq_offsets), states.data_ptr(), _ptr(dL_dh),
